@@ -35,6 +35,8 @@ SGEMM_ERR_INDEX = 8
 MATH_FP32 = 0
 MATH_TF32 = 1
 
+DTYPE_F32, DTYPE_BF16 = 0, 1
+
 KERNEL_NONE, KERNEL_SCALE, KERNEL_FFMA, KERNEL_TF32 = 0, 1, 2, 3
 
 OPT_FORCE_CONFIG = 1
@@ -62,6 +64,13 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class VocabPlan(ctypes.Structure):
+    """Mirror of ``sgemm_vocab_plan_t``."""
+
+    _fields_ = [("pieces", ctypes.c_int), ("piece", ctypes.c_int), ("launches", ctypes.c_int),
+                ("workspace_bytes", ctypes.c_longlong)]
 
 
 class SgemmError(RuntimeError):
@@ -92,6 +101,11 @@ _SIGNATURES = {
     "sgemm_status_string": ([_I], ctypes.c_char_p),
     "sgemm_run_splitk_static": ([_I, _I, _I, _F, _P, _I, _P, _I, _F, _P, _I, _I, _P, _P], _I),
     "sgemm_run_min2": ([_P, _I, _I, _I, _F, _P, _I, _P, _I, _F, _P, _I, _P, _P, _P], _I),
+    "sgemm_xent": ([_P, _I, _I, _I, _I, _P, _I, _P, _I, _P, _F, _P, _P, _P], _I),
+    "sgemm_xent_grad": ([_P, _I, _I, _I, _I, _P, _I, _P, _I, _P, _F, _P, _P, _F, _P, _I, _P, _I, _P], _I),
+    "sgemm_distill": ([_P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, _F, _P, _P, _P], _I),
+    "sgemm_distill_grad": ([_P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, _F, _P, _P, _F, _P, _I, _P, _I, _P], _I),
+    "sgemm_vocab_plan": ([_I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(VocabPlan)], _I),
     "sgemm_ladder_run": ([_I, _I, _I, _I, _F, _P, _P, _F, _P, _P], _I),
 }
 
@@ -133,6 +147,15 @@ def plan(M, N, K, lda=None, ldb=None, ldc=None, align_flags=7, num_sms=152, math
     ldc = max(1, N) if ldc is None else ldc
     _check(library().sgemm_plan(M, N, K, lda, ldb, ldc, align_flags, num_sms, math_mode, ctypes.byref(p)),
            "sgemm_plan")
+    return p
+
+
+def vocab_plan(T, V, D, dtype=DTYPE_BF16, n=0, grad=False, align_flags=3, num_sms=152,
+               math_mode=MATH_FP32) -> VocabPlan:
+    """Host-only: what a vocabulary loss (``n`` teacher entries, 0 for the cross entropy) or its gradients would do."""
+    p = VocabPlan()
+    _check(library().sgemm_vocab_plan(T, V, D, dtype, n, int(bool(grad)), align_flags, num_sms, math_mode,
+                                      ctypes.byref(p)), "sgemm_vocab_plan")
     return p
 
 
@@ -192,6 +215,40 @@ def _matrix_arg(t, rows, cols, name):
         raise ValueError(f"{name} must be row-major with unit column stride")
     ld = t.stride(0) if rows > 1 else max(1, cols)
     return t.data_ptr(), max(ld, 1)
+
+
+def _rows_arg(t, rows, cols, name, like=None):
+    """(pointer, row stride) of a row-major float32 or bfloat16 CUDA matrix (of ``like``'s type and device)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be a 2-D torch.float32 or torch.bfloat16 tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if rows > 0 and cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major with unit column stride")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else max(1, cols))
+
+
+def _list_arg(t, shape, dtype, name, like):
+    """Pointer of a packed tensor of one value per token, or pointer and row stride of one of several."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != like.device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {like.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if len(shape) == 1:
+        if shape[0] > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name} must be packed")
+        return t.data_ptr()
+    if shape[0] > 0 and shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major with unit column stride")
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else max(1, shape[1]))
 
 
 class Sgemm:
@@ -257,6 +314,129 @@ class Sgemm:
         _check(library().sgemm_run_min2(self._h, M, N, K, alpha, pa, lda, pb, ldb, beta, pc, ldc, vals.data_ptr(),
                                         ij.data_ptr(), self._stream(stream)), "sgemm_run_min2")
         return vals, ij
+
+    def _projection(self, H, W):
+        """Checked operands of a vocabulary loss: (T, V, D, dtype), H and W arguments."""
+        import torch
+
+        for t, name in ((H, "H"), (W, "W")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 2:
+                raise TypeError(f"{name} must be a 2-D torch tensor")
+        T, D = H.shape
+        V = W.shape[0]
+        pw, ldw = _rows_arg(W, V, D, "W")
+        ph, ldh = _rows_arg(H, T, D, "H", like=W)
+        if W.device.index != self.device:
+            raise ValueError(f"the operands are on {W.device}, the handle on cuda:{self.device}")
+        dtype = DTYPE_BF16 if W.dtype == torch.bfloat16 else DTYPE_F32
+        return (T, V, D, dtype), (ph, ldh, pw, ldw)
+
+    def _on(self, stream):
+        """Context in which new tensors belong to the stream that the call runs on."""
+        import contextlib
+
+        import torch
+
+        if stream is None:
+            return contextlib.nullcontext()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        return torch.cuda.stream(stream)
+
+    def _entries(self, ids, logits, T, like):
+        """Checked teacher entries: (n, ids, logits, row stride)."""
+        import torch
+
+        n = ids.shape[1] if isinstance(ids, torch.Tensor) and ids.dim() == 2 else 0
+        if n < 1:
+            raise ValueError("ids must be a 2-D tensor with at least one entry per token")
+        pi, ldi = _list_arg(ids, (T, n), torch.int64, "ids", like)
+        pl, ldl = _list_arg(logits, (T, n), torch.float32, "logits", like)
+        if ldi != ldl:
+            raise ValueError(f"ids and logits have different row strides ({ldi} and {ldl})")
+        return n, pi, pl, ldi
+
+    def _loss_outputs(self, T, like, stream):
+        import torch
+
+        with self._on(stream):
+            return (torch.empty(T, dtype=torch.float32, device=like.device),
+                    torch.empty(T, dtype=torch.float32, device=like.device))
+
+    def _grad_outputs(self, H, W, dH, dW, beta, need_dH, need_dW, stream):
+        """(dH, dW, arguments): outputs are made where they are asked for and not given."""
+        import torch
+
+        if beta != 0.0 and ((need_dH and dH is None) or (need_dW and dW is None)):
+            raise ValueError("beta != 0 adds to given gradients: pass dH and dW")
+        with self._on(stream):
+            dH = (torch.empty(H.shape, dtype=H.dtype, device=H.device) if dH is None else dH) if need_dH else None
+            dW = (torch.empty(W.shape, dtype=W.dtype, device=W.device) if dW is None else dW) if need_dW else None
+        args = ()
+        for t, like, name in ((dH, H, "dH"), (dW, W, "dW")):
+            args += (None, 0) if t is None else _rows_arg(t, like.shape[0], like.shape[1], name, like=W)
+        return dH, dW, args
+
+    def xent(self, H, W, labels, scale: float = 1.0, stream=None):
+        """Cross entropy of ``scale * H @ W.T`` against ``labels``, the logits never stored: ``(loss, lse)`` per token.
+
+        H (tokens x width) and W (vocabulary x width): float32 or bfloat16, row-major. labels: int64; a token whose
+        label is outside the vocabulary (-100, say) is masked and has loss 0. loss and lse are float32.
+        """
+        import torch
+
+        (T, V, D, dtype), operands = self._projection(H, W)
+        py = _list_arg(labels, (T,), torch.int64, "labels", W)
+        loss, lse = self._loss_outputs(T, W, stream)
+        _check(library().sgemm_xent(self._h, T, V, D, dtype, *operands, py, scale, loss.data_ptr(), lse.data_ptr(),
+                                    self._stream(stream)), "sgemm_xent")
+        return loss, lse
+
+    def xent_grad(self, H, W, labels, lse, dloss, scale: float = 1.0, dH=None, dW=None, beta: float = 0.0,
+                  need_dH: bool = True, need_dW: bool = True, stream=None):
+        """``(dH, dW)`` of :meth:`xent` (with its ``lse``) for the gradient ``dloss`` of each token's loss.
+
+        Given dH / dW are updated in place: gradient + beta * given. ``need_dH`` / ``need_dW`` False leaves that one
+        out (None), for a head or a trunk that is not trained.
+        """
+        import torch
+
+        (T, V, D, dtype), operands = self._projection(H, W)
+        py = _list_arg(labels, (T,), torch.int64, "labels", W)
+        ps = _list_arg(lse, (T,), torch.float32, "lse", W)
+        pg = _list_arg(dloss, (T,), torch.float32, "dloss", W)
+        dH, dW, outputs = self._grad_outputs(H, W, dH, dW, beta, need_dH, need_dW, stream)
+        _check(library().sgemm_xent_grad(self._h, T, V, D, dtype, *operands, py, scale, ps, pg, beta, *outputs,
+                                         self._stream(stream)), "sgemm_xent_grad")
+        return dH, dW
+
+    def distill(self, H, W, ids, logits, temperature: float = 1.0, stream=None):
+        """Divergence of ``softmax(H @ W.T / temperature)`` from a teacher known by its top logits: ``(loss, lse)``.
+
+        ids (int64) and logits (float32): one row of entries per token, in any order; an id outside the vocabulary
+        (-1, say) leaves its entry out, a token without entries is masked. The loss carries the factor
+        temperature**2, lse is that of the logits divided by the temperature.
+        """
+        (T, V, D, dtype), operands = self._projection(H, W)
+        n, pi, pl, ldn = self._entries(ids, logits, T, W)
+        loss, lse = self._loss_outputs(T, W, stream)
+        _check(library().sgemm_distill(self._h, T, V, D, dtype, *operands, n, pi, pl, ldn, temperature,
+                                       loss.data_ptr(), lse.data_ptr(), self._stream(stream)), "sgemm_distill")
+        return loss, lse
+
+    def distill_grad(self, H, W, ids, logits, lse, dloss, temperature: float = 1.0, dH=None, dW=None,
+                     beta: float = 0.0, need_dH: bool = True, need_dW: bool = True, stream=None):
+        """``(dH, dW)`` of :meth:`distill` (with its ``lse``); arguments as for :meth:`xent_grad`."""
+        import torch
+
+        (T, V, D, dtype), operands = self._projection(H, W)
+        n, pi, pl, ldn = self._entries(ids, logits, T, W)
+        ps = _list_arg(lse, (T,), torch.float32, "lse", W)
+        pg = _list_arg(dloss, (T,), torch.float32, "dloss", W)
+        dH, dW, outputs = self._grad_outputs(H, W, dH, dW, beta, need_dH, need_dW, stream)
+        _check(library().sgemm_distill_grad(self._h, T, V, D, dtype, *operands, n, pi, pl, ldn, temperature, ps, pg,
+                                            beta, *outputs, self._stream(stream)), "sgemm_distill_grad")
+        return dH, dW
 
     def run_ptr(self, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream=None) -> int:
         """Direct C-ABI call with raw device pointers; returns the status (no exception)."""

@@ -1,0 +1,178 @@
+// Row kernels of the vocabulary losses: the teacher's entries made into sorted
+// target tables, the losses put together from the tiles' partial softmax
+// statistics, and the end of the sum of dH. All of them are bound by a few
+// megabytes of traffic beside the products.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "sgemm_internal.h"
+#include "vocab_internal.h"
+
+namespace sgemm_impl {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+
+// One block per token. q = softmax over the entries that count of logit * scale,
+// then the entries in ascending order of id: an entry's place is the number of
+// entries before it (n <= 1024, so n^2 comparisons in shared memory are less work
+// than the passes of a sort), equal ids staying in the given order. What is left
+// out sorts to the end as kNoTarget with q = 0.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
+vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const float *__restrict__ logits, long long ldn,
+                     float scale, int *__restrict__ tid, float *__restrict__ tq, float *__restrict__ tlogq)
+{
+    __shared__ int s_id[SGEMM_DISTILL_MAX_ENTRIES];
+    __shared__ float s_x[SGEMM_DISTILL_MAX_ENTRIES];
+    __shared__ float s_red[2][THREADS / 32];
+    const long long row = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float best = -kInf;
+    for (int j = threadIdx.x; j < n; j += THREADS) {
+        const long long id = ids[row * ldn + j];
+        const bool counts = id >= 0 && id < V;
+        const float x = counts ? logits[row * ldn + j] * scale : -kInf;
+        s_id[j] = counts && x > -kInf ? static_cast<int>(id) : kNoTarget;
+        if (x != x) s_id[j] = static_cast<int>(id);  // a NaN logit stays and makes the token's loss NaN
+        s_x[j] = x;
+        best = x != x ? x : fmaxf(best, x);
+    }
+    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) s_red[0][warp] = best;
+    __syncthreads();
+    best = s_red[0][0];
+    for (int w = 1; w < THREADS / 32; ++w) best = fmaxf(best, s_red[0][w]);
+    float sum = 0.0f;
+    for (int j = threadIdx.x; j < n; j += THREADS)
+        if (s_id[j] != kNoTarget) sum += expf(s_x[j] - best);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < THREADS / 32; ++w) sum += s_red[1][w];
+    const float logsum = logf(sum);
+    for (int j = threadIdx.x; j < n; j += THREADS) {
+        const int id = s_id[j];
+        int at = 0;
+        for (int i = 0; i < n; ++i) at += s_id[i] < id || (s_id[i] == id && i < j);
+        const bool counts = id != kNoTarget;
+        const float t = s_x[j] - best;
+        tid[row * n + at] = id;
+        tq[row * n + at] = counts ? expf(t) / sum : 0.0f;
+        tlogq[row * n + at] = counts ? t - logsum : 0.0f;
+    }
+}
+
+// 8 tokens per block, 32 lanes for each: lane l folds the (max, sum) pairs of tile
+// columns l, l + 32, ... (8 tokens' pairs are 64 contiguous bytes), then the lanes
+// fold theirs; a fixed order, so the result does not depend on scheduling.
+constexpr int kCombineRows = 8;
+
+__device__ __forceinline__ void fold(float &m, float &s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2);
+    if (top == -kInf) {  // nothing but -infinity so far (both sums 0), or NaN, which fmaxf leaves out of m but s holds
+        s += s2;
+        return;
+    }
+    s = s * expf(m - top) + s2 * expf(m2 - top);
+    m = top;
+}
+
+__global__ void __launch_bounds__(kCombineRows * 32)
+vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ part, int parts,
+                     const float *__restrict__ zt, float mult, float *__restrict__ loss, float *__restrict__ lse)
+{
+    __shared__ float sm[32][kCombineRows + 1], ss[32][kCombineRows + 1];
+    const int r = threadIdx.x % kCombineRows, l = threadIdx.x / kCombineRows;
+    const long long first = static_cast<long long>(blockIdx.x) * kCombineRows;
+    float m = -kInf, s = 0.0f;
+    if (first + r < T)
+        for (int c = l; c < parts; c += 32) {
+            const float2 x = part[static_cast<long long>(c) * T + first + r];
+            fold(m, s, x.x, x.y);
+        }
+    sm[l][r] = m;
+    ss[l][r] = s;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // a warp per token
+    const long long row = first + warp;
+    if (row >= T) return;
+    m = sm[lane][warp];
+    s = ss[lane][warp];
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const bool low = (lane & o) == 0;  // both lanes fold in the same order
+        float am = low ? m : m2, as = low ? s : s2;
+        fold(am, as, low ? m2 : m, low ? s2 : s);
+        m = am;
+        s = as;
+    }
+    const float total = m + logf(s);
+    float sum = 0.0f;
+    if (t.labels != nullptr) {
+        const long long y = t.labels[row];
+        if (lane == 0 && y >= 0 && y < V) sum = total - zt[row];
+    } else {
+        for (int j = lane; j < t.n; j += 32) {
+            const float q = t.q[row * t.n + j];
+            if (t.id[row * t.n + j] != kNoTarget && q != 0.0f)  // q of 0: the limit of q log q
+                sum += q * (t.logq[row * t.n + j] + (total - zt[row * t.n + j]));
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 0) {
+        lse[row] = total;
+        loss[row] = mult * sum;
+    }
+}
+
+template <typename E>
+__global__ void vocab_finish_kernel(int rows, int cols, const float *__restrict__ acc, long long ldacc, float beta,
+                                    E *__restrict__ dst, long long ldd)
+{
+    const long long total = static_cast<long long>(rows) * cols;
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+        const long long r = i / cols, c = i % cols;
+        E *d = dst + r * ldd + c;
+        float x = acc != nullptr ? acc[r * ldacc + c] : 0.0f;
+        if (beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
+        *d = static_cast<E>(x);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, const float *logits, long long ldn,
+                                 float scale, int *tid, float *tq, float *tlogq, cudaStream_t stream)
+{
+    vocab_targets_kernel<128><<<T, 128, 0, stream>>>(V, n, ids, logits, ldn, scale, tid, tq, tlogq);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
+                                 float mult, float *loss, float *lse, cudaStream_t stream)
+{
+    vocab_combine_kernel<<<(T + kCombineRows - 1) / kCombineRows, kCombineRows * 32, 0, stream>>>(
+        T, V, t, part, parts, zt, mult, loss, lse);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, float beta, void *dst,
+                                long long ldd, int dtype, int num_sms, cudaStream_t stream)
+{
+    const long long blocks = (static_cast<long long>(rows) * cols + 1023) / 1024;
+    const int grid = static_cast<int>(std::min<long long>(std::max<long long>(blocks, 1), 8LL * num_sms));
+    if (dtype == SGEMM_DTYPE_BF16)
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, beta, static_cast<__nv_bfloat16 *>(dst),
+                                                      ldd);
+    else
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, beta, static_cast<float *>(dst), ldd);
+    return cudaGetLastError();
+}
+
+}  // namespace sgemm_impl
