@@ -110,6 +110,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// As tma_load_2d for a 3-D map.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // Thread-block clusters (PTX ISA "Cluster of Cooperative Thread Arrays",
 // mapa, ld.shared::cluster, barrier.cluster): used by the TF32 CTA-pair kernel
 // and by the FFMA kernel's split-K reduced within a cluster.

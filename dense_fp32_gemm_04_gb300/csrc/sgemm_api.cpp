@@ -14,6 +14,7 @@
 #include "handle.h"
 #include "planner.h"
 #include "sgemm_internal.h"
+#include "vocab_internal.h"
 
 using namespace sgemm_impl;
 
@@ -460,7 +461,8 @@ int sgemm_create_for_device(int dev, sgemm_handle_t *out)
         return SGEMM_ERR_CUDA;
     }
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
-    if (ffma_set_attributes() != cudaSuccess || tf32_set_attributes() != cudaSuccess) {
+    if (ffma_set_attributes() != cudaSuccess || tf32_set_attributes() != cudaSuccess ||
+        vocab_set_attributes() != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return SGEMM_ERR_CUDA;
@@ -468,6 +470,8 @@ int sgemm_create_for_device(int dev, sgemm_handle_t *out)
     {
         const int pairs = tf32_pair_max_pairs();
         h->tf32_pairs = pairs > 0 ? std::min(pairs, sms / 2) : -1;
+        const int vocab = vocab_max_pairs();
+        h->vocab_pairs = vocab > 0 ? std::min(vocab, sms / 2) : -1;
     }
     if (cudaMalloc(&h->d_status, 256) != cudaSuccess || cudaMemset(h->d_status, 0, 256) != cudaSuccess ||
         cudaMalloc(&h->min2_cand, min2_candidate_bytes(8 * sms)) != cudaSuccess) {

@@ -42,7 +42,8 @@ enum : int {
     kWhereIdxSkReduce = 29,   // stream-K reduction's partial-tile reads
     kWhereIdxSplitReduce = 30,// split-K reduction's slice reads
     kWhereIdxTf32Copy = 33,   // TF32 TMA tile coordinate
-    kWhereIdxTf32Store = 34   // TF32 store to C or to a partial tile
+    kWhereIdxTf32Store = 34,  // TF32 store to C or to a partial tile
+    kWhereIdxVocabDz = 35     // vocabulary losses: columns of dZ outside a piece's buffer
 };
 
 // Everything the FFMA mainloop needs besides the two tensor maps.

@@ -43,7 +43,7 @@ VocabProblem problem(const Call &c)
     auto rows16 = [size](const void *p, long long ld) { return aligned(p, 16) && ld * size % 16 == 0; };
     const int align = (rows16(c.H, c.ldh) ? 1 : 0) | (rows16(c.W, c.ldw) ? 2 : 0);
     return VocabProblem{c.T, c.V, c.D, c.dtype, c.n, c.dH != nullptr, c.dW != nullptr, align, c.h->num_sms,
-                        c.h->math_mode};
+                        c.h->math_mode, c.h->vocab_pairs};
 }
 
 int check(const Call &c, bool grad)
@@ -72,23 +72,56 @@ int check(const Call &c, bool grad)
     return SGEMM_OK;
 }
 
-// Targets (the distillation's tables are made first) and the parameters every tile kernel shares.
-int begin(const Call &c, const VocabLayout &w, VocabTileParams *p)
+// Map of a (rows x cols) bfloat16 matrix of `parts` parts, in boxes of 64 x 64.
+int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int cols, int rows, long long ld, int parts,
+             long long part)
+{
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2u, static_cast<cuuint64_t>(part) * 2u};
+    cuuint32_t box[3] = {64, 64, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
+}
+
+// The map of H or W: the caller's matrix, or its parts, which are made first.
+int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src, int rows, int ld, long long off,
+                long long ldp, CUtensorMap *map)
+{
+    if (!copy) {
+        return make_map(c.h, map, src, c.D, rows, ld, 1, static_cast<long long>(ld) * rows);
+    }
+    void *dst = static_cast<char *>(c.h->workspace) + off;
+    const long long part = rows * ldp;
+    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.h->num_sms, c.stream) != cudaSuccess)
+        return SGEMM_ERR_LAUNCH;
+    return make_map(c.h, map, dst, c.D, rows, ldp, w.parts, part);
+}
+
+// Operands, targets (the distillation's tables are made first) and what every launch of the call shares.
+int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, CUtensorMap *tmH, CUtensorMap *tmW)
 {
     char *ws = static_cast<char *>(c.h->workspace);
+    int rc;
+    if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, tmH)) != SGEMM_OK) return rc;
+    if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, tmW)) != SGEMM_OK) return rc;
     p->T = c.T;
     p->V = c.V;
     p->D = c.D;
-    p->H = c.H;
-    p->W = c.W;
-    p->ldh = c.ldh;
-    p->ldw = c.ldw;
+    p->dtype = c.dtype;
+    p->parts = w.parts;
+    p->products = w.products;
+    // Segments (vocab_kernels.cu): 512 deep for the logits, 256 for FP32 operands, whole for sums rounded to bfloat16.
+    p->seg_z = w.parts == 1 ? 8 : 4;
+    p->seg_g = w.parts == 1 ? 1 << 24 : 4;
     p->scale = c.scale;
     p->lse = c.lse;
     p->dloss = c.dloss;
     p->gmult = c.mult * c.scale;
-    p->v0 = 0;
-    p->vn = c.V;
+    p->status = c.h->d_status;
+    p->timeout_ns = c.h->timeout_ns;
     p->t.labels = c.labels;
     p->t.n = c.n > 0 ? c.n : 1;
     if (c.n > 0) {
@@ -103,6 +136,8 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p)
     return SGEMM_OK;
 }
 
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
 int run_loss(const Call &c)
 {
     int rc = check(c, false);
@@ -110,16 +145,20 @@ int run_loss(const Call &c)
     if (c.T == 0) return SGEMM_OK;
     DeviceGuard g(c.h->device);
     if (!g.ok) return SGEMM_ERR_CUDA;
-    VocabProblem q = problem(c);
-    const VocabLayout w = vocab_layout(q);
+    const VocabLayout w = vocab_layout(problem(c));
     if ((rc = ensure_workspace(c.h, static_cast<size_t>(w.pub.workspace_bytes), c.stream)) != SGEMM_OK) return rc;
     char *ws = static_cast<char *>(c.h->workspace);
     VocabTileParams p{};
-    if ((rc = begin(c, w, &p)) != SGEMM_OK) return rc;
+    CUtensorMap tmH, tmW;
+    if ((rc = begin(c, w, &p, &tmH, &tmW)) != SGEMM_OK) return rc;
+    p.z_kind = kVocabLoss;
+    p.z_tm = ceil_div(c.T, 128 * w.ctas);
+    p.z_tn = ceil_div(c.V, kVocabBN);
+    p.z_items = static_cast<long long>(p.z_tm) * p.z_tn;
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
-    if (launch_vocab_forward(p, c.dtype, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    if (launch_vocab_combine(c.T, c.V, p.t, p.part, w.parts, p.zt, c.mult, c.loss, c.lse_out, c.stream) != cudaSuccess)
+    if (launch_vocab_tiles(tmH, tmW, tmW, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    if (launch_vocab_combine(c.T, c.V, p.t, p.part, w.stat_cols, p.zt, c.mult, c.loss, c.lse_out, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;
 }
@@ -132,30 +171,58 @@ int run_grad(const Call &c)
     DeviceGuard g(c.h->device);
     if (!g.ok) return SGEMM_ERR_CUDA;
     if (c.T == 0) {
-        if (c.dW != nullptr && launch_vocab_finish(c.V, c.D, nullptr, 0, c.beta, c.dW, c.lddw, c.dtype, c.h->num_sms,
-                                                   c.stream) != cudaSuccess)
+        if (c.dW != nullptr && launch_vocab_finish(c.V, c.D, nullptr, 0, 0, 0, c.beta, c.dW, c.lddw, c.dtype,
+                                                   c.h->num_sms, c.stream) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
         return SGEMM_OK;
     }
-    VocabProblem q = problem(c);
-    const VocabLayout w = vocab_layout(q);
+    const VocabLayout w = vocab_layout(problem(c));
     if ((rc = ensure_workspace(c.h, static_cast<size_t>(w.pub.workspace_bytes), c.stream)) != SGEMM_OK) return rc;
     char *ws = static_cast<char *>(c.h->workspace);
     VocabTileParams p{};
-    if ((rc = begin(c, w, &p)) != SGEMM_OK) return rc;
-    p.G = reinterpret_cast<float *>(ws + w.g_off);
+    CUtensorMap tmH, tmW;
+    if ((rc = begin(c, w, &p, &tmH, &tmW)) != SGEMM_OK) return rc;
+    const int bm = 128 * w.ctas, tm = ceil_div(c.T, bm), tn = ceil_div(c.D, kVocabBN);
+    const int elem = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
+    p.z_kind = kVocabDz;
+    p.z_tm = tm;
     p.ldg = w.ldg;
-    float *acc = reinterpret_cast<float *>(ws + w.acc_off);
-    for (int i = 0; i < w.pub.pieces; ++i) {
-        p.v0 = i * w.pub.piece;
-        p.vn = c.V - p.v0 < w.pub.piece ? c.V - p.v0 : w.pub.piece;
-        if (launch_vocab_dz(p, c.dtype, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-        if (c.dH != nullptr && launch_vocab_dh(p, c.dtype, acc, i == 0, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-        if (c.dW != nullptr && launch_vocab_dw(p, c.dtype, c.beta, c.dW, c.lddw, c.stream) != cudaSuccess)
-            return SGEMM_ERR_LAUNCH;
+    p.g_part = c.T * w.ldg;
+    p.dW = c.dW;
+    p.lddw = c.lddw;
+    p.dw_vec = aligned(c.dW, 4 * elem) && c.lddw % 4 == 0;
+    p.beta = c.beta;
+    p.dw_tn = tn;
+    p.dh_tm = tm;
+    p.dh_tn = tn;
+    p.dh_kb = w.dh_kb;
+    p.acc = reinterpret_cast<float *>(ws + w.acc_off);
+    p.ldacc = w.ldacc;
+    p.acc_split = c.T * w.ldacc;
+    // Launch i: the dH and dW tiles of piece i - 1 and the dZ tiles of piece i.
+    for (int i = 0; i <= w.pub.pieces; ++i) {
+        CUtensorMap tmG = tmW;
+        p.dh_items = p.dw_items = p.z_items = 0;
+        if (i > 0) {
+            p.g_v0 = (i - 1) * w.pub.piece;
+            p.g_vn = c.V - p.g_v0 < w.pub.piece ? c.V - p.g_v0 : w.pub.piece;
+            const int splits = ceil_div(ceil_div(p.g_vn, kVocabBK), w.dh_kb > 0 ? w.dh_kb : 1);
+            if (c.dH != nullptr) p.dh_items = static_cast<long long>(tm) * tn * splits;
+            if (c.dW != nullptr) p.dw_items = static_cast<long long>(ceil_div(p.g_vn, bm)) * tn;
+            p.acc_add = i > 1;
+            if ((rc = make_map(c.h, &tmG, ws + w.g_off[(i - 1) & 1], p.g_vn, c.T, w.ldg, w.parts, p.g_part)) != SGEMM_OK)
+                return rc;
+        }
+        if (i < w.pub.pieces) {
+            p.z_v0 = i * w.pub.piece;
+            p.z_tn = ceil_div(c.V - p.z_v0 < w.pub.piece ? c.V - p.z_v0 : w.pub.piece, kVocabBN);
+            p.z_items = static_cast<long long>(tm) * p.z_tn;
+            p.Gw = reinterpret_cast<__nv_bfloat16 *>(ws + w.g_off[i & 1]);
+        }
+        if (launch_vocab_tiles(tmH, tmW, tmG, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
-    if (c.dH != nullptr &&
-        launch_vocab_finish(c.T, c.D, acc, c.D, c.beta, c.dH, c.lddh, c.dtype, c.h->num_sms, c.stream) != cudaSuccess)
+    if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, p.acc, w.ldacc, p.acc_split, w.dh_splits, c.beta, c.dH, c.lddh,
+                                               c.dtype, c.h->num_sms, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;
 }

@@ -4,6 +4,8 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/sgemm.h"
@@ -25,6 +27,9 @@ struct VocabTargets {
     const float *logq;        // [T][n]
 };
 
+// Tile shape: 256 columns per tile, slabs of 64 along K; 128 rows per CTA.
+constexpr int kVocabBN = 256, kVocabBK = 64;
+
 struct VocabProblem {
     int T, V, D;
     int dtype;  // sgemm_dtype_t
@@ -33,18 +38,24 @@ struct VocabProblem {
     int align_flags;
     int num_sms;
     int math_mode;
+    int pairs;  // CTA pairs resident at once (0: num_sms / 2; < 0: none)
 };
 
-// Byte offsets of the parts of the workspace (parts that a call does not use are empty).
+// What a call does, and the byte offsets of the parts of its workspace (those a call does not use are empty).
 struct VocabLayout {
     sgemm_vocab_plan_t pub;
+    int ctas;      // CTAs per worker: 2 = pairs computing 256 x 256 tiles, 1 = 128 x 256
+    int workers;
+    int parts, products;  // bfloat16 parts of an operand, products of parts
+    bool copy_h, copy_w;  // operand goes into the workspace as parts
+    long long h_off, ldh, w_off, ldw;      // bytes, elements
     long long tid_off, tq_off, tlogq_off;  // target tables [T][n]
     long long zt_off;                      // logits at the targets, [T][n]
-    long long part_off;                    // (max, sum of exp) per token and tile column, [parts][T]
-    int parts;                             // tile columns of V
-    long long g_off;                       // dZ of one piece
-    long long ldg;
-    long long acc_off;                     // FP32 sum of dH over the pieces, [T][D]
+    long long part_off;                    // (max, sum of exp) per token and 128 columns, [columns / 128][T]
+    int stat_cols;                         // columns / 128
+    long long g_off[2], ldg;               // dZ of a piece, [parts][T][ldg]; two of them, in turn
+    int dh_splits, dh_kb;                  // dH tiles: parts of a piece along the vocabulary, k-blocks each
+    long long acc_off, ldacc;              // FP32 sums of dH, [dh_splits][T][ldacc]
 };
 
 int validate_vocab(const VocabProblem &q);
@@ -53,34 +64,54 @@ VocabLayout vocab_layout(const VocabProblem &q);
 // Row kernels (vocab_rows.cu).
 cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, const float *logits, long long ldn,
                                  float scale, int *tid, float *tq, float *tlogq, cudaStream_t stream);
-// lse and loss of each token from the tile columns' (max, sum) pairs and the logits at its targets.
+// lse and loss of each token from the columns' (max, sum) pairs and the logits at its targets.
 cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
                                  float mult, float *loss, float *lse, cudaStream_t stream);
-// dst = acc + beta * dst (acc == NULL: dst = beta * dst), rows x cols.
-cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, float beta, void *dst,
-                                long long ldd, int dtype, int num_sms, cudaStream_t stream);
+// dst = sum of `splits` FP32 matrices + beta * dst (splits == 0: dst = beta * dst), rows x cols.
+cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
+                                float beta, void *dst, long long ldd, int dtype, int num_sms, cudaStream_t stream);
 
-// Tile kernels (vocab_kernels.cu).
+// Tile kernel (vocab_kernels.cu): one launch's tiles.
+enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };
+
 struct VocabTileParams {
     int T, V, D;
-    const void *H, *W;
-    long long ldh, ldw;
+    int dtype;
+    int parts, products;
+    int seg_z, seg_g;  // k-blocks per accumulator segment
     float scale;
     VocabTargets t;
+    // Z tiles of columns [z_v0, z_v0 + 256 z_tn): the loss, or dZ of one piece
+    int z_kind, z_v0, z_tm, z_tn;
+    long long z_items;
     float2 *part;
     float *zt;
     const float *lse, *dloss;
-    float gmult;       // c * scale
-    int v0, vn;        // this piece of the vocabulary
-    float *G;          // [T][ldg]
-    long long ldg;
+    float gmult;         // c * scale
+    __nv_bfloat16 *Gw;   // dZ written
+    long long ldg, g_part;  // row stride, elements between parts
+    // dH and dW tiles of the piece [g_v0, g_v0 + g_vn), whose dZ an earlier launch left
+    int g_v0, g_vn;
+    int dw_tn;
+    long long dw_items;
+    void *dW;
+    long long lddw;
+    bool dw_vec;  // rows of dW can be written 4 elements at a time
+    float beta;
+    int dh_tm, dh_tn, dh_kb;
+    long long dh_items;
+    float *acc;
+    long long ldacc, acc_split;
+    bool acc_add;  // add to the sums (a later piece)
+    int *status;
+    long long timeout_ns;
 };
-cudaError_t launch_vocab_forward(const VocabTileParams &p, int dtype, cudaStream_t stream);
-cudaError_t launch_vocab_dz(const VocabTileParams &p, int dtype, cudaStream_t stream);
-// acc (+)= dZ * W of the piece; `first`: written, else added to
-cudaError_t launch_vocab_dh(const VocabTileParams &p, int dtype, float *acc, bool first, cudaStream_t stream);
-// dW rows of the piece = dZ^T * H + beta * dW
-cudaError_t launch_vocab_dw(const VocabTileParams &p, int dtype, float beta, void *dW, long long lddw,
-                            cudaStream_t stream);
+cudaError_t vocab_set_attributes();
+int vocab_max_pairs();
+// Maps of H, W and the piece's dZ: (elements of a row, rows, parts), boxes of 64 x 64 x 1, 128-byte swizzle.
+cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
+                               const VocabTileParams &p, int ctas, int workers, cudaStream_t stream);
+cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
+                               long long ldd, long long part, int num_sms, cudaStream_t stream);
 
 }  // namespace sgemm_impl

@@ -1,186 +1,759 @@
-// Tile kernels of the vocabulary losses. Z = scale * H * W^T is computed tile by
-// tile with FP32 FMAs from operands widened to FP32 and leaves a tile either as
-// the softmax statistics of its columns (and the logits at the targets), or as dZ
-// for the two products of the gradients.
+// Tile kernel of the vocabulary losses on the 5th-generation tensor cores. One
+// persistent kernel computes all three products of bfloat16 operands with FP32
+// accumulation, 128 x 256 tiles per CTA or 256 x 256 tiles per CTA pair:
+//   Z   = scale * H W^T   A = H (T x D, K-major), B = W (V x D, K-major); leaves
+//                         the tile as softmax statistics (loss), or as dZ in
+//                         bfloat16 parts (dz). Z itself is never stored.
+//   dW  = dZ^T H          A = dZ (T x piece, read MN-major), B = H (MN-major)
+//   dH  = dZ W            A = dZ (K-major), B = W (MN-major), split along the
+//                         vocabulary into partial sums that vocab_finish adds.
+// One launch of a gradient call holds the dH and dW tiles of one piece of the
+// vocabulary and the dZ tiles of the next, so the partial last round of one
+// product is filled by another's tiles.
+//
+// FP32 operands are sums of bfloat16 parts (vocab_parts_kernel); a product of
+// three parts each is the six bfloat16 products down to 2^-16 of the leading
+// one, small ones first: the same loop over more slabs.
+//
+// Accumulation: the tensor core truncates its FP32 accumulator at every K = 16
+// step (measured: rel. error 4.4e-6 at K = 4096, all of it toward zero), which a
+// logit of 12 would show in its loss. So a tile's K range is cut into segments
+// (512 deep for Z, 256 deep in every product of FP32 operands); the epilogue
+// warps add the segments in registers, rounded to nearest, while the next ones
+// run. Products whose result is rounded to bfloat16 (dW, dH of bfloat16
+// operands) are one segment: 2^-9 hides what truncation loses.
+//
+// Warps of a CTA (three warpgroups): 0 TMA producer, 1 MMA issuer (rank 0 of a
+// pair), 2 and 3 idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4) and
+// columns 128 (w / 8) of the accumulator, so a thread holds 128 columns of one
+// row. That takes more registers than an even share: the first warpgroup hands
+// most of its own over (setmaxnreg). Ring and accumulator barriers are those of the TF32 kernel (tf32_kernels.cu): full /
+// empty per stage, acc_full / acc_empty per accumulator, all waits bounded.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cstdint>
+
+#include "device_ptx.cuh"
 #include "sgemm_internal.h"
+#include "tcgen05_ptx.cuh"
 #include "vocab_internal.h"
 
 namespace sgemm_impl {
 namespace {
 
-constexpr int TILE = 64, BK = 16, THREADS = 256;
+using namespace sgemm_dev;
+
+constexpr int kTimeoutCode = 5 << 16;
+constexpr int kLayoutCode = 7 << 16;
+constexpr int BK = kVocabBK;   // 64 bfloat16 = 128 bytes, one swizzle row
+constexpr int BN = kVocabBN;   // 256 accumulator columns
+constexpr int MMA_K = 16;
+constexpr int BOX_BYTES = 64 * 64 * 2;  // every copy: 64 rows of 64 elements
+constexpr int THREADS = 384;
+constexpr int EPI_WARPS = 8;
+// Registers per thread: at launch (the most that 384 threads can have), and after the warpgroups' exchange.
+constexpr int REGS_LAUNCH = 168, REGS_ISSUE = 72, REGS_EPILOGUE = 216;
+static_assert(REGS_ISSUE + 2 * REGS_EPILOGUE <= 3 * REGS_LAUNCH, "an exchange above the launch's registers never ends");
+constexpr int COLS = 128;      // accumulator columns of one epilogue thread
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int kPitch = 33;     // floats between staged rows: row- and column-wise accesses without bank conflicts
+constexpr int kStagingBytes = EPI_WARPS * 32 * kPitch * 4;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
-// acc[i][j] of C rows 4 ty + i, columns 4 tx + j of the tile at (m0, n0):
-// sum over k of A(m, k) B(n, k), element (r, k) of an operand at base + r * sr + k * sk.
-template <typename EA, typename EB>
-__device__ void tile_product(const EA *A, long long a_sr, long long a_sk, int m0, int M, const EB *B, long long b_sr,
-                             long long b_sk, int n0, int N, int K, float (&acc)[4][4])
+template <int CTAS>
+struct Shape {
+    static constexpr int BM = 128 * CTAS;
+    static constexpr int CTA_N = BN / CTAS;  // columns of B staged per CTA
+    static constexpr int STAGES = CTAS == 2 ? 6 : 4;
+    static constexpr int A_BYTES = 128 * BK * 2;
+    static constexpr int B_BYTES = CTA_N * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 512 + kStagingBytes;
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+template <int STAGES>
+struct Bars {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    uint32_t ring_offset;
+    int abort_flag;
+    int issued[STAGES];
+};
+static_assert(sizeof(Bars<6>) <= 512, "barrier block");
+
+template <int STAGES>
+__device__ __forceinline__ void raise_abort(Bars<STAGES> *b, const VocabTileParams &p, int code)
 {
-    __shared__ float sa[BK][TILE + 1], sb[BK][TILE + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int k0 = 0; k0 < K; k0 += BK) {
-        for (int i = threadIdx.x; i < BK * TILE; i += THREADS) {
-            // consecutive threads along the operand's contiguous axis
-            const int ra = a_sk == 1 ? i / BK : i % TILE, ka = a_sk == 1 ? i % BK : i / TILE;
-            const int rb = b_sk == 1 ? i / BK : i % TILE, kb = b_sk == 1 ? i % BK : i / TILE;
-            sa[ka][ra] = m0 + ra < M && k0 + ka < K ? static_cast<float>(A[(m0 + ra) * a_sr + (k0 + ka) * a_sk]) : 0.0f;
-            sb[kb][rb] = n0 + rb < N && k0 + kb < K ? static_cast<float>(B[(n0 + rb) * b_sr + (k0 + kb) * b_sk]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < BK; ++k) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = sa[k][4 * ty + i];
-                b[i] = sb[k][4 * tx + i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-        }
-        __syncthreads();
+    volatile int *f = &b->abort_flag;
+    if (!*f) {
+        *f = 1;
+        report_status(p.status, code);
     }
 }
 
-template <typename E, bool DZ>
-__global__ void __launch_bounds__(THREADS) vocab_z_kernel(const VocabTileParams p)
+// One tile of a launch: rows from m0, columns from n0, k-blocks [kb0, kb1).
+struct Item {
+    int kind, m0, n0, kb0, kb1, split;
+};
+
+// Item u: the dH tiles (split s of all tiles, then of the next split), then the
+// dW tiles (along D first: they share their slice of dZ), then the Z tiles (in
+// groups of 16 tile rows, along T first: they share their rows of W, and the
+// group's rows of H stay in the L2).
+__device__ __forceinline__ bool item_at(const VocabTileParams &p, long long u, int bm, Item &w)
 {
-    const int n0 = p.v0 + blockIdx.x * TILE, m0 = blockIdx.y * TILE, nend = p.v0 + p.vn;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    tile_product(static_cast<const E *>(p.H), p.ldh, 1LL, m0, p.T, static_cast<const E *>(p.W), p.ldw, 1LL, n0, nend, p.D,
-                 acc);
-    for (int i = 0; i < 4; ++i) {
-        const long long row = m0 + 4 * ty + i;
-        const bool live = row < p.T;  // every thread takes part in the shuffles
-        float z[4], m = -kInf, s = 0.0f;
-        for (int j = 0; j < 4; ++j) {
-            const int col = n0 + 4 * tx + j;
-            z[j] = col < nend ? p.scale * acc[i][j] : -kInf;
-            m = fmaxf(m, z[j]);
-        }
-        float dz[4] = {};
-        if (!DZ) {
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == -kInf ? 0.0f : m;
-            for (int j = 0; j < 4; ++j) s += expf(z[j] - base);
-            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (live && tx == 0) p.part[static_cast<long long>(blockIdx.x) * p.T + row] = make_float2(m, s);
-        }
-        if (!live) continue;
-        float g = 0.0f;
-        if (DZ) {
-            const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
-            const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
-            if (used) {
-                g = p.gmult * p.dloss[row];
-                const float l = p.lse[row];
-                for (int j = 0; j < 4; ++j) dz[j] = g * expf(z[j] - l);
+    if (u < p.dh_items) {
+        const int tiles = p.dh_tm * p.dh_tn, r = static_cast<int>(u % tiles);
+        w.kind = kVocabDh;
+        w.split = static_cast<int>(u / tiles);
+        w.m0 = r % p.dh_tm * bm;
+        w.n0 = r / p.dh_tm * BN;
+        w.kb0 = w.split * p.dh_kb;
+        w.kb1 = min(w.kb0 + p.dh_kb, (p.g_vn + BK - 1) / BK);
+        return true;
+    }
+    u -= p.dh_items;
+    w.split = 0;
+    w.kb0 = 0;
+    if (u < p.dw_items) {
+        w.kind = kVocabDw;
+        w.m0 = static_cast<int>(u / p.dw_tn) * bm;
+        w.n0 = static_cast<int>(u % p.dw_tn) * BN;
+        w.kb1 = (p.T + BK - 1) / BK;
+        return true;
+    }
+    u -= p.dw_items;
+    if (u >= p.z_items) return false;
+    constexpr int GROUP = 16;
+    const int group = static_cast<int>(u / (GROUP * p.z_tn)), rows = min(GROUP, p.z_tm - group * GROUP);
+    const int r = static_cast<int>(u - static_cast<long long>(group) * GROUP * p.z_tn);
+    w.kind = p.z_kind;
+    w.m0 = (group * GROUP + r % rows) * bm;
+    w.n0 = r / rows * BN;
+    w.kb1 = (p.D + BK - 1) / BK;
+    return true;
+}
+
+__device__ __forceinline__ int segment_blocks(const VocabTileParams &p, int kind)
+{
+    return kind == kVocabDw || kind == kVocabDh ? p.seg_g : p.seg_z;
+}
+
+// Parts of A and B in product i (0..5) of the six; a call of fewer parts runs the last ones.
+__device__ __forceinline__ int part_a(int i) { return (0x001102 >> (4 * i)) & 3; }
+__device__ __forceinline__ int part_b(int i) { return (0x010120 >> (4 * i)) & 3; }
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The thread's 128 columns of one row, written where they belong through the
+// warp's staging area, so that the stores of a warp run along rows: 32 columns at
+// a time, thread l's row into staged row l, then 8 lanes per row (16-byte rows) or
+// 32 lanes along one row (any alignment).
+enum { kToUser, kToAcc, kAddToAcc };
+
+template <int MODE, typename E>
+__device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg, int lane, E *dst, long long ld, int rows,
+                                           int cols, bool vec, float beta)
+{
+#pragma unroll
+    for (int cb = 0; cb < COLS / 32; ++cb) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stg[lane * kPitch + i] = acc[cb * 32 + i];
+        __syncwarp();
+        if (cb * 32 < cols) {
+            if (vec) {
+                const int sub = lane >> 3, c = cb * 32 + 4 * (lane & 7);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + sub;
+                    const float *s = stg + r * kPitch + 4 * (lane & 7);
+                    float x[4] = {s[0], s[1], s[2], s[3]};
+                    if (r >= rows || c >= cols) continue;
+                    E *d = dst + r * ld + c;
+                    if (c + 3 < cols) {
+                        if constexpr (MODE == kAddToAcc) {
+                            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(d), "f"(x[0]), "f"(x[1]),
+                                         "f"(x[2]), "f"(x[3])
+                                         : "memory");
+                        } else if constexpr (sizeof(E) == 4) {
+                            if (MODE == kToUser && beta != 0.0f) {
+                                const float4 o = *reinterpret_cast<const float4 *>(d);
+                                x[0] = fmaf(beta, o.x, x[0]);
+                                x[1] = fmaf(beta, o.y, x[1]);
+                                x[2] = fmaf(beta, o.z, x[2]);
+                                x[3] = fmaf(beta, o.w, x[3]);
+                            }
+                            *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
+                        } else {
+                            __nv_bfloat162 *d2 = reinterpret_cast<__nv_bfloat162 *>(d);
+                            if (beta != 0.0f) {
+                                const float2 o0 = __bfloat1622float2(d2[0]), o1 = __bfloat1622float2(d2[1]);
+                                x[0] = fmaf(beta, o0.x, x[0]);
+                                x[1] = fmaf(beta, o0.y, x[1]);
+                                x[2] = fmaf(beta, o1.x, x[2]);
+                                x[3] = fmaf(beta, o1.y, x[3]);
+                            }
+                            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+                            *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(y);
+                        }
+                    } else {
+                        for (int e = 0; e < 4; ++e)
+                            if (c + e < cols) {
+                                if (MODE == kAddToAcc || (MODE == kToUser && beta != 0.0f))
+                                    x[e] = fmaf(MODE == kAddToAcc ? 1.0f : beta, static_cast<float>(d[e]), x[e]);
+                                d[e] = static_cast<E>(x[e]);
+                            }
+                    }
+                }
+            } else {
+                const int c = cb * 32 + lane;
+#pragma unroll 4
+                for (int r = 0; r < 32; ++r) {
+                    float x = stg[r * kPitch + lane];
+                    if (r < rows && c < cols) {
+                        E *d = dst + r * ld + c;
+                        if (MODE == kToUser && beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
+                        *d = static_cast<E>(x);
+                    }
+                }
             }
         }
-        for (int e = 0; e < p.t.n; ++e) {
-            const long long id = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n + e];
-            const float q = p.t.labels != nullptr ? 1.0f : p.t.q[row * p.t.n + e];
+        __syncwarp();
+    }
+}
+
+// Targets of one row: the entries with ids in [c0, c0 + 128) in turn. f(column - c0, entry, weight).
+template <typename F>
+__device__ __forceinline__ void for_targets(const VocabTileParams &p, long long row, bool live, int c0, F f)
+{
+    if (p.t.labels != nullptr) {
+        if (!live) return;
+        const long long y = p.t.labels[row];
+        if (y >= c0 && y < c0 + COLS && y < p.V) f(static_cast<int>(y - c0), 0, 1.0f);
+        return;
+    }
+    if (!live) return;
+    const int *id = p.t.id + row * p.t.n;
+    int lo = 0, hi = p.t.n;  // first entry with id >= c0
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (id[mid] < c0)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    for (; lo < p.t.n; ++lo) {
+        const int y = id[lo];
+        if (y >= c0 + COLS || y >= p.V) break;  // kNoTarget ends the list too
+        f(y - c0, lo, p.t.q[row * p.t.n + lo]);
+    }
+}
+
+// Z tile of a loss call: (max, sum of exp) of the thread's columns, and the logits at its targets.
+__device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
+{
+    const bool live = row < p.T;
+    const int cols = p.V - c0;  // columns of the vocabulary from c0 on
+    float m = -kInf;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+        z[i] = i < cols ? z[i] * p.scale : -kInf;
+        m = fmaxf(m, z[i]);
+    }
+    const float base = m == -kInf ? 0.0f : m;
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < COLS; i += 4) {
+        s0 += exp2_approx((z[i] - base) * kLog2e);
+        s1 += exp2_approx((z[i + 1] - base) * kLog2e);
+        s2 += exp2_approx((z[i + 2] - base) * kLog2e);
+        s3 += exp2_approx((z[i + 3] - base) * kLog2e);
+    }
+    if (live) p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(m, (s0 + s1) + (s2 + s3));
+    for_targets(p, row, live, c0, [&](int at, int entry, float) {
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
+        p.zt[row * p.t.n + entry] = x;
+    });
+}
+
+// Z tile of a gradient call: dZ = g (exp(z - lse) - q), in bfloat16 parts. The last part is rounded to
+// nearest, as the earlier ones are: their remainders are exact in FP32.
+template <int PARTS>
+__device__ __forceinline__ void store_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c)
+{
+    __nv_bfloat16 *dst = p.Gw + row * p.ldg + c;
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+#pragma unroll
+        for (int i = 0; i < COLS; i += 8) {
+            __nv_bfloat162 y[4];
+#pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int col = n0 + 4 * tx + j;
-                if (id != col || col >= nend) continue;
-                if (DZ)
-                    dz[j] -= g * q;
+                y[j] = __floats2bfloat162_rn(z[i + 2 * j], z[i + 2 * j + 1]);
+                if (part + 1 < PARTS) {
+                    const float2 back = __bfloat1622float2(y[j]);
+                    z[i + 2 * j] -= back.x;
+                    z[i + 2 * j + 1] -= back.y;
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst + i) = *reinterpret_cast<const uint4 *>(y);
+        }
+        dst += p.g_part;
+    }
+}
+
+__device__ __forceinline__ void leave_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
+{
+    if (row >= p.T) return;
+    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
+    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
+    const float g = used ? p.gmult * p.dloss[row] : 0.0f, l = p.lse[row];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+        const float e = g * exp2_approx((z[i] * p.scale - l) * kLog2e);
+        z[i] = used ? e : 0.0f;  // a masked token's dZ is 0 whatever its logits are
+    }
+    for_targets(p, row, true, c0, [&](int at, int, float q) {
+        const float t = g * q;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) z[i] -= i == at ? t : 0.0f;
+    });
+    // ldg covers whole tiles; columns past the vocabulary hold what the products' copies never read
+    const int c = c0 - p.z_v0;
+    if (!index_ok(c >= 0 && c + COLS <= p.ldg, p.status, kWhereIdxVocabDz)) return;
+    if (p.parts == 1)
+        store_dz<1>(p, z, row, c);
+    else if (p.parts == 2)
+        store_dz<2>(p, z, row, c);
+    else
+        store_dz<3>(p, z, row, c);
+}
+
+// Producer thread: this CTA's part of each stage, in boxes of 64 rows x 64 elements.
+template <int CTAS>
+__device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, uint32_t a_base,
+                                        uint32_t b_base, const CUtensorMap &tmH, const CUtensorMap &tmW,
+                                        const CUtensorMap &tmG, uint32_t rank, int worker, int workers)
+{
+    using S = Shape<CTAS>;
+    constexpr int STAGES = S::STAGES;
+    constexpr bool PAIR = CTAS == 2;
+    volatile int *abort_flag = &bars->abort_flag;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Item w;
+    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+        const bool z = w.kind == kVocabLoss || w.kind == kVocabDz;
+        const CUtensorMap *ta = z ? &tmH : &tmG;
+        const CUtensorMap *tb = w.kind == kVocabDw ? &tmH : &tmW;
+        const bool a_k = w.kind != kVocabDw, b_k = z;  // K-major: K along the map's rows
+        const int a_r = w.m0 + static_cast<int>(rank) * 128;
+        const int b_r = w.n0 + static_cast<int>(rank) * S::CTA_N + (z ? p.z_v0 : 0);
+        const int b_k0 = w.kind == kVocabDh ? p.g_v0 : 0;
+        const int seg = segment_blocks(p, w.kind);
+        for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg) {
+            const int s1 = min(s0 + seg, w.kb1);
+            for (int pr = 6 - p.products; ok && pr < 6; ++pr) {
+                const int pa = part_a(pr), pb = part_b(pr);
+                for (int kb = s0; kb < s1; ++kb) {
+                    if (!mbar_wait_bounded(smem_addr(&bars->empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
+                        raise_abort(bars, p, kTimeoutCode | kWhereProducerEmpty);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a_dst = a_base + stage * S::A_BYTES;
+                    const uint32_t b_dst = b_base + stage * S::B_BYTES;
+                    if (rank == 0) mbar_arrive_expect_tx(smem_addr(&bars->full[stage]), CTAS * S::STAGE_BYTES);
+                    uint32_t full = smem_addr(&bars->full[stage]);
+                    if constexpr (PAIR) full = mapa_shared(full, 0);  // rank 0's barrier
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int x = a_k ? kb * BK : a_r + 64 * j, y = a_k ? a_r + 64 * j : kb * BK;
+                        if constexpr (PAIR)
+                            tma_load_3d_pair(a_dst + j * BOX_BYTES, ta, full, x, y, pa);
+                        else
+                            tma_load_3d(a_dst + j * BOX_BYTES, ta, full, x, y, pa);
+                    }
+#pragma unroll
+                    for (int j = 0; j < S::CTA_N / 64; ++j) {
+                        const int x = b_k ? kb * BK : b_r + 64 * j, y = b_k ? b_r + 64 * j : b_k0 + kb * BK;
+                        if constexpr (PAIR)
+                            tma_load_3d_pair(b_dst + j * BOX_BYTES, tb, full, x, y, pb);
+                        else
+                            tma_load_3d(b_dst + j * BOX_BYTES, tb, full, x, y, pb);
+                    }
+                    bars->issued[stage] = 2 | static_cast<int>(phase);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    }
+    // Drain, as in the TF32 kernel: every issued copy has landed (rank 0's barriers count both
+    // CTAs'), and unless aborted the MMAs that read it have committed.
+    for (int s = 0; s < STAGES; ++s) {
+        const int rec = bars->issued[s];
+        if (!(rec & 2)) continue;
+        const uint32_t par = static_cast<uint32_t>(rec & 1);
+        if (rank == 0 && !mbar_wait_cluster_bounded(smem_addr(&bars->full[s]), par, nullptr, p.timeout_ns)) {
+            report_status(p.status, kTimeoutCode | kWhereDrain);
+            break;
+        }
+        if (!*abort_flag && !mbar_wait_bounded(smem_addr(&bars->empty[s]), par, abort_flag, p.timeout_ns)) {
+            report_status(p.status, kTimeoutCode | kWhereDrain);
+            break;
+        }
+    }
+}
+
+// MMA thread (rank 0 of a pair): four K = 16 steps per slab, a commit per stage and per segment.
+template <int CTAS>
+__device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, uint32_t a_base,
+                                      uint32_t b_base, uint32_t tmem, int worker, int workers)
+{
+    using S = Shape<CTAS>;
+    constexpr int STAGES = S::STAGES;
+    constexpr bool PAIR = CTAS == 2;
+    volatile int *abort_flag = &bars->abort_flag;
+    int stage = 0;
+    uint32_t phase = 0;
+    int it = 0;  // segments so far
+    bool ok = true;
+    Item w;
+    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+        const bool a_mn = w.kind == kVocabDw, b_mn = w.kind == kVocabDw || w.kind == kVocabDh;
+        const uint32_t idesc = idesc_bf16(S::BM, BN, a_mn, b_mn);
+        const int seg = segment_blocks(p, w.kind);
+        for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg, ++it) {
+            const int buf = it & 1;
+            const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
+            if (!mbar_wait_cluster_bounded(smem_addr(&bars->acc_empty[buf]), acc_phase ^ 1u, abort_flag,
+                                           p.timeout_ns)) {
+                raise_abort(bars, p, kTimeoutCode | kWhereAccum);
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * BN);
+            const int slabs = (min(s0 + seg, w.kb1) - s0) * p.products;
+            for (int i = 0; i < slabs; ++i) {
+                if (!mbar_wait_cluster_bounded(smem_addr(&bars->full[stage]), phase, abort_flag, p.timeout_ns)) {
+                    raise_abort(bars, p, kTimeoutCode | kWhereMmaEmpty);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t a_s = a_base + stage * S::A_BYTES;
+                const uint32_t b_s = b_base + stage * S::B_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / MMA_K; ++k) {
+                    // K-major: 16 elements = 32 bytes inside the swizzle row; MN-major: 16 K-rows of 128 bytes
+                    const uint64_t a_desc = a_mn ? smem_desc_mn_sw128(a_s + k * MMA_K * 128, BOX_BYTES)
+                                                 : smem_desc_k_sw128(a_s + k * MMA_K * 2);
+                    const uint64_t b_desc = b_mn ? smem_desc_mn_sw128(b_s + k * MMA_K * 128, BOX_BYTES)
+                                                 : smem_desc_k_sw128(b_s + k * MMA_K * 2);
+                    const uint32_t accumulate = (i | k) != 0 ? 1u : 0u;
+                    if constexpr (PAIR)
+                        mma_bf16_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
+                    else
+                        mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);
+                }
+                if constexpr (PAIR)
+                    mma_commit_pair_both(smem_addr(&bars->empty[stage]));
                 else
-                    p.zt[row * p.t.n + e] = z[j];
+                    mma_commit(smem_addr(&bars->empty[stage]));
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if constexpr (PAIR)
+                mma_commit_pair_both(smem_addr(&bars->acc_full[buf]));
+            else
+                mma_commit(smem_addr(&bars->acc_full[buf]));
+        }
+    }
+    if constexpr (PAIR)
+        mma_commit_pair_local(smem_addr(&bars->mma_done));
+    else
+        mma_commit(smem_addr(&bars->mma_done));
+    if (!mbar_wait_bounded(smem_addr(&bars->mma_done), 0u, nullptr, p.timeout_ns))
+        report_status(p.status, kTimeoutCode | kWhereDrain);
+}
+
+// Epilogue warp: the segments of a tile added up in registers, then the tile left as its kind wants it.
+template <int CTAS>
+__device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, float *staging,
+                                            uint32_t tmem, uint32_t rank, int warp, int lane, int worker, int workers)
+{
+    using S = Shape<CTAS>;
+    constexpr bool PAIR = CTAS == 2;
+    volatile int *abort_flag = &bars->abort_flag;
+    const int quarter = warp & 3, half = warp >> 3;
+    float *stg = staging + (warp - 4) * 32 * kPitch;
+    int it = 0;
+    bool ok = true;
+    Item w;
+    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+        float acc[COLS];
+        const int seg = segment_blocks(p, w.kind);
+        for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
+            const int buf = it & 1;
+            const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
+            ok = mbar_wait_cluster_bounded(smem_addr(&bars->acc_full[buf]), acc_phase, abort_flag, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0) raise_abort(bars, p, kTimeoutCode | kWhereAccum);
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(buf * BN + half * COLS);
+#pragma unroll
+            for (int cb = 0; cb < COLS / 32; ++cb) {
+                uint32_t v[32];
+                tmem_ld_32(t + cb * 32, v);
+                tmem_wait_ld_32(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    acc[cb * 32 + i] = s0 == w.kb0 ? __uint_as_float(v[i]) : acc[cb * 32 + i] + __uint_as_float(v[i]);
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    mbar_arrive_cluster(mapa_shared(smem_addr(&bars->acc_empty[buf]), 0));  // rank 0's
+                else
+                    mbar_arrive(smem_addr(&bars->acc_empty[buf]));
             }
         }
-        if (DZ)
-            for (int j = 0; j < 4; ++j) {
-                const int col = n0 + 4 * tx + j;
-                if (col < nend) p.G[row * p.ldg + col - p.v0] = dz[j];
-            }
+        if (!ok) break;
+        const int r0 = w.m0 + static_cast<int>(rank) * 128 + quarter * 32;  // the warp's first row
+        const int c0 = w.n0 + half * COLS;
+        if (w.kind == kVocabLoss) {
+            leave_loss(p, acc, r0 + lane, p.z_v0 + c0);
+        } else if (w.kind == kVocabDz) {
+            leave_dz(p, acc, r0 + lane, p.z_v0 + c0);
+        } else if (w.kind == kVocabDw) {
+            const int rows = p.g_vn - r0, cols = p.D - c0;
+            const long long at = static_cast<long long>(p.g_v0 + r0) * p.lddw + c0;
+            if (p.dtype == SGEMM_DTYPE_BF16)
+                write_rows<kToUser>(acc, stg, lane, static_cast<__nv_bfloat16 *>(p.dW) + at, p.lddw, rows, cols,
+                                    p.dw_vec, p.beta);
+            else
+                write_rows<kToUser>(acc, stg, lane, static_cast<float *>(p.dW) + at, p.lddw, rows, cols, p.dw_vec,
+                                    p.beta);
+        } else {
+            float *dst = p.acc + w.split * p.acc_split + static_cast<long long>(r0) * p.ldacc + c0;
+            if (p.acc_add)
+                write_rows<kAddToAcc>(acc, stg, lane, dst, p.ldacc, p.T - r0, p.D - c0, true, 0.0f);
+            else
+                write_rows<kToAcc>(acc, stg, lane, dst, p.ldacc, p.T - r0, p.D - c0, true, 0.0f);
+        }
     }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(THREADS) vocab_dh_kernel(const VocabTileParams p, float *out, bool first)
+template <int CTAS>
+__global__ void __launch_bounds__(THREADS, 1)
+vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+             const __grid_constant__ CUtensorMap tmG, const __grid_constant__ VocabTileParams p)
 {
-    const int n0 = blockIdx.x * TILE, m0 = blockIdx.y * TILE;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    tile_product(p.G, p.ldg, 1LL, m0, p.T, static_cast<const E *>(p.W) + p.v0 * p.ldw, 1LL, p.ldw, n0, p.D, p.vn, acc);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long row = m0 + 4 * ty + i, col = n0 + 4 * tx + j;
-            if (row < p.T && col < p.D) {
-                float *d = out + row * p.D + col;
-                *d = first ? acc[i][j] : *d + acc[i][j];
-            }
+    using S = Shape<CTAS>;
+    constexpr int STAGES = S::STAGES;
+    constexpr bool PAIR = CTAS == 2;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t a_base = smem_addr(smem);
+    const uint32_t b_base = a_base + STAGES * S::A_BYTES;
+    Bars<STAGES> *bars = reinterpret_cast<Bars<STAGES> *>(smem + STAGES * S::STAGE_BYTES);
+    float *staging = reinterpret_cast<float *>(smem + STAGES * S::STAGE_BYTES + 512);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (PAIR && cluster_size() != 2) {
+        if (threadIdx.x == 0) report_status(p.status, kLayoutCode | kWherePairLayout);
+        return;
+    }
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const int worker = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+    const int workers = PAIR ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_addr(&bars->full[s]), 1);
+            mbar_init(smem_addr(&bars->empty[s]), 1);
+            bars->issued[s] = 0;
         }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&bars->acc_full[b]), 1);
+            mbar_init(smem_addr(&bars->acc_empty[b]), EPI_WARPS * CTAS);
+        }
+        mbar_init(smem_addr(&bars->mma_done), 1);
+        bars->abort_flag = 0;
+        bars->ring_offset = a_base;
+        fence_barrier_init();
+        prefetch_tensormap(&tmH);
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmG);
+    }
+    if (warp == 0) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_addr(&bars->tmem_base), TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_addr(&bars->tmem_base), TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are initialised before any copy or arrive targets them
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    bool same_layout = true;
+    if constexpr (PAIR) {
+        constexpr uint32_t kDescAddrMask = 0x3FFFFu;
+        const uint32_t peer_ring = ld_shared_cluster_u32(mapa_shared(smem_addr(&bars->ring_offset), rank ^ 1u));
+        same_layout = ((peer_ring ^ a_base) & kDescAddrMask) == 0;
+        if (!same_layout && threadIdx.x == 0) raise_abort(bars, p, kLayoutCode | kWherePairLayout);
+    }
+
+    // Where the pair's layouts differ both CTAs see it: no copies, no MMAs.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
+        if (same_layout && warp == 0 && lane == 0)
+            produce<CTAS>(p, bars, a_base, b_base, tmH, tmW, tmG, rank, worker, workers);
+        else if (same_layout && warp == 1 && lane == 0 && rank == 0)
+            issue<CTAS>(p, bars, a_base, b_base, tmem, worker, workers);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPILOGUE));
+        if (same_layout) leave_tiles<CTAS>(p, bars, staging, tmem, rank, warp, lane, worker, workers);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still use its barriers, stages or TMEM
+    tc_fence_after_sync();
+    if (warp == 0) {
+        __syncwarp();
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem, TMEM_COLS);
+        else
+            tmem_dealloc(tmem, TMEM_COLS);
+    }
 }
 
+// Operand of FP32 or bfloat16 at any row stride -> `parts` bfloat16 parts at a 16-byte row stride:
+// x = x0 + x1 + x2, each the remainder rounded to nearest (three parts hold all 24 bits). A value that
+// would round to infinity is truncated instead; infinities and NaN stay in the first part.
 template <typename E>
-__global__ void __launch_bounds__(THREADS)
-vocab_dw_kernel(const VocabTileParams p, float beta, E *__restrict__ dW, long long lddw)
+__global__ void vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, int parts,
+                                   __nv_bfloat16 *__restrict__ dst, long long ldd, long long part)
 {
-    const int n0 = blockIdx.x * TILE, m0 = blockIdx.y * TILE;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    tile_product(p.G, 1LL, p.ldg, m0, p.vn, static_cast<const E *>(p.H), 1LL, p.ldh, n0, p.D, p.T, acc);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long row = m0 + 4 * ty + i, col = n0 + 4 * tx + j;
-            if (row < p.vn && col < p.D) {
-                E *d = dW + (p.v0 + row) * lddw + col;
-                *d = static_cast<E>(beta != 0.0f ? fmaf(beta, static_cast<float>(*d), acc[i][j]) : acc[i][j]);
+    const int pairs = static_cast<int>(ldd / 2);
+    const long long total = static_cast<long long>(rows) * pairs;
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+        const long long r = i / pairs;
+        const int c = static_cast<int>(i % pairs) * 2;
+        float x[2];
+        for (int e = 0; e < 2; ++e) x[e] = c + e < cols ? static_cast<float>(src[r * ld + c + e]) : 0.0f;
+        __nv_bfloat162 *d = reinterpret_cast<__nv_bfloat162 *>(dst + r * ldd + c);
+        for (int k = 0; k < parts; ++k) {
+            __nv_bfloat16 y[2];
+            for (int e = 0; e < 2; ++e) {
+                const bool fine = fabsf(x[e]) < kInf;
+                y[e] = __float2bfloat16_rn(x[e]);
+                if (fine && __hisinf(y[e])) y[e] = __float2bfloat16_rz(x[e]);
+                x[e] = fine ? x[e] - __bfloat162float(y[e]) : 0.0f;
             }
+            *d = __nv_bfloat162(y[0], y[1]);
+            d += part / 2;
         }
+    }
 }
 
-unsigned tiles(int x) { return static_cast<unsigned>((x + TILE - 1) / TILE); }
+template <int CTAS>
+cudaError_t set_attributes()
+{
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, vocab_kernel<CTAS>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;  // the exchange of registers could not end
+    return cudaFuncSetAttribute(vocab_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CTAS>::SMEM);
+}
 
 }  // namespace
 
-cudaError_t launch_vocab_forward(const VocabTileParams &p, int dtype, cudaStream_t stream)
+cudaError_t vocab_set_attributes()
 {
-    const dim3 grid(tiles(p.vn), tiles(p.T));
-    if (dtype == SGEMM_DTYPE_BF16)
-        vocab_z_kernel<__nv_bfloat16, false><<<grid, THREADS, 0, stream>>>(p);
-    else
-        vocab_z_kernel<float, false><<<grid, THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    const cudaError_t e = set_attributes<1>();
+    return e != cudaSuccess ? e : set_attributes<2>();
 }
 
-cudaError_t launch_vocab_dz(const VocabTileParams &p, int dtype, cudaStream_t stream)
+int vocab_max_pairs()
 {
-    const dim3 grid(tiles(p.vn), tiles(p.T));
-    if (dtype == SGEMM_DTYPE_BF16)
-        vocab_z_kernel<__nv_bfloat16, true><<<grid, THREADS, 0, stream>>>(p);
-    else
-        vocab_z_kernel<float, true><<<grid, THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Shape<2>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, vocab_kernel<2>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return clusters;
 }
 
-cudaError_t launch_vocab_dh(const VocabTileParams &p, int dtype, float *acc, bool first, cudaStream_t stream)
+cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
+                               const VocabTileParams &p, int ctas, int workers, cudaStream_t stream)
 {
-    const dim3 grid(tiles(p.D), tiles(p.T));
-    if (dtype == SGEMM_DTYPE_BF16)
-        vocab_dh_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p, acc, first);
-    else
-        vocab_dh_kernel<float><<<grid, THREADS, 0, stream>>>(p, acc, first);
-    return cudaGetLastError();
+    const long long items = p.dh_items + p.dw_items + p.z_items;
+    const int n = static_cast<int>(std::min<long long>(items, workers));
+    if (ctas == 2)
+        return launch_kernel_cluster(false, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream, tmH,
+                                     tmW, tmG, p);
+    return launch_kernel(false, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, tmH, tmW, tmG, p);
 }
 
-cudaError_t launch_vocab_dw(const VocabTileParams &p, int dtype, float beta, void *dW, long long lddw,
-                            cudaStream_t stream)
+cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
+                               long long ldd, long long part, int num_sms, cudaStream_t stream)
 {
-    const dim3 grid(tiles(p.D), tiles(p.vn));
+    const long long blocks = (static_cast<long long>(rows) * (ldd / 2) + 1023) / 1024;
+    const int grid = static_cast<int>(std::min<long long>(std::max<long long>(blocks, 1), 16LL * num_sms));
+    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst);
     if (dtype == SGEMM_DTYPE_BF16)
-        vocab_dw_kernel<<<grid, THREADS, 0, stream>>>(p, beta, static_cast<__nv_bfloat16 *>(dW), lddw);
+        vocab_parts_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, parts, d,
+                                                     ldd, part);
     else
-        vocab_dw_kernel<<<grid, THREADS, 0, stream>>>(p, beta, static_cast<float *>(dW), lddw);
+        vocab_parts_kernel<<<grid, 256, 0, stream>>>(static_cast<const float *>(src), ld, rows, cols, parts, d, ldd,
+                                                     part);
     return cudaGetLastError();
 }
 

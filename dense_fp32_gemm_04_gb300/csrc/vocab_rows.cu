@@ -130,16 +130,18 @@ vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ pa
     }
 }
 
+// The partial sums of a dH element in split order, then beta * dst, rounded once.
 template <typename E>
-__global__ void vocab_finish_kernel(int rows, int cols, const float *__restrict__ acc, long long ldacc, float beta,
-                                    E *__restrict__ dst, long long ldd)
+__global__ void vocab_finish_kernel(int rows, int cols, const float *__restrict__ acc, long long ldacc, long long split,
+                                    int splits, float beta, E *__restrict__ dst, long long ldd)
 {
     const long long total = static_cast<long long>(rows) * cols;
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
     for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
         const long long r = i / cols, c = i % cols;
         E *d = dst + r * ldd + c;
-        float x = acc != nullptr ? acc[r * ldacc + c] : 0.0f;
+        float x = 0.0f;
+        for (int s = 0; s < splits; ++s) x += acc[s * split + r * ldacc + c];
         if (beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
         *d = static_cast<E>(x);
     }
@@ -162,16 +164,17 @@ cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const floa
     return cudaGetLastError();
 }
 
-cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, float beta, void *dst,
-                                long long ldd, int dtype, int num_sms, cudaStream_t stream)
+cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
+                                float beta, void *dst, long long ldd, int dtype, int num_sms, cudaStream_t stream)
 {
     const long long blocks = (static_cast<long long>(rows) * cols + 1023) / 1024;
     const int grid = static_cast<int>(std::min<long long>(std::max<long long>(blocks, 1), 8LL * num_sms));
     if (dtype == SGEMM_DTYPE_BF16)
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, beta, static_cast<__nv_bfloat16 *>(dst),
-                                                      ldd);
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, split, splits, beta,
+                                                      static_cast<__nv_bfloat16 *>(dst), ldd);
     else
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, beta, static_cast<float *>(dst), ldd);
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, split, splits, beta,
+                                                      static_cast<float *>(dst), ldd);
     return cudaGetLastError();
 }
 
