@@ -1,5 +1,6 @@
 // C ABI of the vocabulary losses: argument checks, workspace, launches.
 // Declarations and contracts: include/sgemm_vocab.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -95,7 +96,7 @@ int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src,
     }
     void *dst = static_cast<char *>(c.h->workspace) + off;
     const long long part = rows * ldp;
-    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.h->num_sms, c.stream) != cudaSuccess)
+    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return make_map(c.h, map, dst, c.D, rows, ldp, w.parts, part);
 }
@@ -154,7 +155,7 @@ int run_loss(const Call &c)
     p.z_kind = kVocabLoss;
     p.z_tm = ceil_div(c.T, 128 * w.ctas);
     p.z_tn = ceil_div(c.V, kVocabBN);
-    p.z_items = static_cast<long long>(p.z_tm) * p.z_tn;
+    p.z_items = p.z_tm * p.z_tn;
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
     if (launch_vocab_tiles(tmH, tmW, tmW, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
@@ -172,7 +173,7 @@ int run_grad(const Call &c)
     if (!g.ok) return SGEMM_ERR_CUDA;
     if (c.T == 0) {
         if (c.dW != nullptr && launch_vocab_finish(c.V, c.D, nullptr, 0, 0, 0, c.beta, c.dW, c.lddw, c.dtype,
-                                                   c.h->num_sms, c.stream) != cudaSuccess)
+                                                   c.stream) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
         return SGEMM_OK;
     }
@@ -207,8 +208,8 @@ int run_grad(const Call &c)
             p.g_v0 = (i - 1) * w.pub.piece;
             p.g_vn = c.V - p.g_v0 < w.pub.piece ? c.V - p.g_v0 : w.pub.piece;
             const int splits = ceil_div(ceil_div(p.g_vn, kVocabBK), w.dh_kb > 0 ? w.dh_kb : 1);
-            if (c.dH != nullptr) p.dh_items = static_cast<long long>(tm) * tn * splits;
-            if (c.dW != nullptr) p.dw_items = static_cast<long long>(ceil_div(p.g_vn, bm)) * tn;
+            if (c.dH != nullptr) p.dh_items = tm * tn * splits;
+            if (c.dW != nullptr) p.dw_items = ceil_div(p.g_vn, bm) * tn;
             p.acc_add = i > 1;
             if ((rc = make_map(c.h, &tmG, ws + w.g_off[(i - 1) & 1], p.g_vn, c.T, w.ldg, w.parts, p.g_part)) != SGEMM_OK)
                 return rc;
@@ -216,13 +217,16 @@ int run_grad(const Call &c)
         if (i < w.pub.pieces) {
             p.z_v0 = i * w.pub.piece;
             p.z_tn = ceil_div(c.V - p.z_v0 < w.pub.piece ? c.V - p.z_v0 : w.pub.piece, kVocabBN);
-            p.z_items = static_cast<long long>(tm) * p.z_tn;
+            p.z_items = tm * p.z_tn;
             p.Gw = reinterpret_cast<__nv_bfloat16 *>(ws + w.g_off[i & 1]);
         }
+        const int others = p.dw_items + p.z_items, rem = p.dh_items % w.workers;
+        const int cost = vocab_cost(c.dW != nullptr ? c.T : c.D);
+        p.dh_extra = p.dh_items > 0 && rem > 0 ? std::min((w.dh_kb + cost / 2) / cost, others / (w.workers - rem)) : 0;
         if (launch_vocab_tiles(tmH, tmW, tmG, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
     if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, p.acc, w.ldacc, p.acc_split, w.dh_splits, c.beta, c.dH, c.lddh,
-                                               c.dtype, c.h->num_sms, c.stream) != cudaSuccess)
+                                               c.dtype, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;
 }

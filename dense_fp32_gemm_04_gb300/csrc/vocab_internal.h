@@ -58,6 +58,9 @@ struct VocabLayout {
     long long acc_off, ldacc;              // FP32 sums of dH, [dh_splits][T][ldacc]
 };
 
+// K-blocks that a tile of `rows` rows (or D columns) along K counts for: no fewer than its epilogue takes.
+inline int vocab_cost(int k) { return k > 6 * kVocabBK ? (k + kVocabBK - 1) / kVocabBK : 6; }
+
 int validate_vocab(const VocabProblem &q);
 VocabLayout vocab_layout(const VocabProblem &q);
 
@@ -69,7 +72,7 @@ cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const floa
                                  float mult, float *loss, float *lse, cudaStream_t stream);
 // dst = sum of `splits` FP32 matrices + beta * dst (splits == 0: dst = beta * dst), rows x cols.
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
-                                float beta, void *dst, long long ldd, int dtype, int num_sms, cudaStream_t stream);
+                                float beta, void *dst, long long ldd, int dtype, cudaStream_t stream);
 
 // Tile kernel (vocab_kernels.cu): one launch's tiles.
 enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };
@@ -83,7 +86,7 @@ struct VocabTileParams {
     VocabTargets t;
     // Z tiles of columns [z_v0, z_v0 + 256 z_tn): the loss, or dZ of one piece
     int z_kind, z_v0, z_tm, z_tn;
-    long long z_items;
+    int z_items;
     float2 *part;
     float *zt;
     const float *lse, *dloss;
@@ -93,13 +96,14 @@ struct VocabTileParams {
     // dH and dW tiles of the piece [g_v0, g_v0 + g_vn), whose dZ an earlier launch left
     int g_v0, g_vn;
     int dw_tn;
-    long long dw_items;
+    int dw_items;
     void *dW;
     long long lddw;
     bool dw_vec;  // rows of dW can be written 4 elements at a time
     float beta;
     int dh_tm, dh_tn, dh_kb;
-    long long dh_items;
+    int dh_items;
+    int dh_extra;  // other tiles for a worker that has one dH tile fewer
     float *acc;
     long long ldacc, acc_split;
     bool acc_add;  // add to the sums (a later piece)
@@ -112,6 +116,6 @@ int vocab_max_pairs();
 cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
                                const VocabTileParams &p, int ctas, int workers, cudaStream_t stream);
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
-                               long long ldd, long long part, int num_sms, cudaStream_t stream);
+                               long long ldd, long long part, cudaStream_t stream);
 
 }  // namespace sgemm_impl

@@ -104,37 +104,48 @@ struct Item {
     int kind, m0, n0, kb0, kb1, split;
 };
 
-// Item u: the dH tiles (split s of all tiles, then of the next split), then the
-// dW tiles (along D first: they share their slice of dZ), then the Z tiles (in
-// groups of 16 tile rows, along T first: they share their rows of W, and the
+// Item i of a worker. First its dH tiles (tile t, split s of all tiles, then the
+// next split), which are the longest: W workers take them in turn, and those left
+// with one fewer take dh_extra other tiles each in its place. Then the others in
+// turn: the dW tiles (along D first: they share their slice of dZ), and the Z tiles
+// (in groups of 16 tile rows, along T first: they share their rows of W, and the
 // group's rows of H stay in the L2).
-__device__ __forceinline__ bool item_at(const VocabTileParams &p, long long u, int bm, Item &w)
+__device__ __forceinline__ bool item_at(const VocabTileParams &p, int i, int worker, int workers, int bm, Item &w)
 {
-    if (u < p.dh_items) {
-        const int tiles = p.dh_tm * p.dh_tn, r = static_cast<int>(u % tiles);
+    const int turns = p.dh_items / workers, rem = p.dh_items - turns * workers;
+    const int mine = turns + (worker < rem ? 1 : 0);
+    if (i < mine) {
+        const int u = worker + i * workers, tiles = p.dh_tm * p.dh_tn, r = u % tiles;
         w.kind = kVocabDh;
-        w.split = static_cast<int>(u / tiles);
+        w.split = u / tiles;
         w.m0 = r % p.dh_tm * bm;
         w.n0 = r / p.dh_tm * BN;
         w.kb0 = w.split * p.dh_kb;
         w.kb1 = min(w.kb0 + p.dh_kb, (p.g_vn + BK - 1) / BK);
         return true;
     }
-    u -= p.dh_items;
+    i -= mine;
+    const int few = workers - rem;  // workers with one dH tile fewer (all of them where rem is 0: then dh_extra is 0)
+    int u;
+    if (worker >= rem && i < p.dh_extra) {
+        u = worker - rem + i * few;
+    } else {
+        if (worker >= rem) i -= p.dh_extra;
+        u = p.dh_extra * few + (worker >= rem ? worker - rem : worker + few) + i * workers;
+    }
     w.split = 0;
     w.kb0 = 0;
     if (u < p.dw_items) {
         w.kind = kVocabDw;
-        w.m0 = static_cast<int>(u / p.dw_tn) * bm;
-        w.n0 = static_cast<int>(u % p.dw_tn) * BN;
+        w.m0 = u / p.dw_tn * bm;
+        w.n0 = u % p.dw_tn * BN;
         w.kb1 = (p.T + BK - 1) / BK;
         return true;
     }
     u -= p.dw_items;
     if (u >= p.z_items) return false;
     constexpr int GROUP = 16;
-    const int group = static_cast<int>(u / (GROUP * p.z_tn)), rows = min(GROUP, p.z_tm - group * GROUP);
-    const int r = static_cast<int>(u - static_cast<long long>(group) * GROUP * p.z_tn);
+    const int group = u / (GROUP * p.z_tn), rows = min(GROUP, p.z_tm - group * GROUP), r = u - group * GROUP * p.z_tn;
     w.kind = p.z_kind;
     w.m0 = (group * GROUP + r % rows) * bm;
     w.n0 = r / rows * BN;
@@ -358,7 +369,7 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
     uint32_t phase = 0;
     bool ok = true;
     Item w;
-    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+    for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool z = w.kind == kVocabLoss || w.kind == kVocabDz;
         const CUtensorMap *ta = z ? &tmH : &tmG;
         const CUtensorMap *tb = w.kind == kVocabDw ? &tmH : &tmW;
@@ -438,7 +449,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
     int it = 0;  // segments so far
     bool ok = true;
     Item w;
-    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+    for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool a_mn = w.kind == kVocabDw, b_mn = w.kind == kVocabDw || w.kind == kVocabDh;
         const uint32_t idesc = idesc_bf16(S::BM, BN, a_mn, b_mn);
         const int seg = segment_blocks(p, w.kind);
@@ -454,7 +465,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * BN);
             const int slabs = (min(s0 + seg, w.kb1) - s0) * p.products;
-            for (int i = 0; i < slabs; ++i) {
+            for (int j = 0; j < slabs; ++j) {
                 if (!mbar_wait_cluster_bounded(smem_addr(&bars->full[stage]), phase, abort_flag, p.timeout_ns)) {
                     raise_abort(bars, p, kTimeoutCode | kWhereMmaEmpty);
                     ok = false;
@@ -470,7 +481,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
                                                  : smem_desc_k_sw128(a_s + k * MMA_K * 2);
                     const uint64_t b_desc = b_mn ? smem_desc_mn_sw128(b_s + k * MMA_K * 128, BOX_BYTES)
                                                  : smem_desc_k_sw128(b_s + k * MMA_K * 2);
-                    const uint32_t accumulate = (i | k) != 0 ? 1u : 0u;
+                    const uint32_t accumulate = (j | k) != 0 ? 1u : 0u;
                     if constexpr (PAIR)
                         mma_bf16_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
                     else
@@ -513,7 +524,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
     int it = 0;
     bool ok = true;
     Item w;
-    for (long long u = worker; ok && item_at(p, u, S::BM, w); u += workers) {
+    for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         float acc[COLS];
         const int seg = segment_blocks(p, w.kind);
         for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
@@ -662,34 +673,64 @@ vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CU
     }
 }
 
-// Operand of FP32 or bfloat16 at any row stride -> `parts` bfloat16 parts at a 16-byte row stride:
+// Operand of FP32 or bfloat16 at any row stride -> PARTS bfloat16 parts at a 16-byte row stride:
 // x = x0 + x1 + x2, each the remainder rounded to nearest (three parts hold all 24 bits). A value that
-// would round to infinity is truncated instead; infinities and NaN stay in the first part.
-template <typename E>
-__global__ void vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, int parts,
-                                   __nv_bfloat16 *__restrict__ dst, long long ldd, long long part)
+// would round to infinity is truncated instead; infinities and NaN stay in the first part. 64 threads
+// per row, N neighbouring elements each: 8 where rows can be read 16 bytes at a time, else 2.
+template <typename E, int PARTS, int N>
+__global__ void __launch_bounds__(256)
+vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, __nv_bfloat16 *__restrict__ dst,
+                   long long ldd, long long part)
 {
-    const int pairs = static_cast<int>(ldd / 2);
-    const long long total = static_cast<long long>(rows) * pairs;
-    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-        const long long r = i / pairs;
-        const int c = static_cast<int>(i % pairs) * 2;
-        float x[2];
-        for (int e = 0; e < 2; ++e) x[e] = c + e < cols ? static_cast<float>(src[r * ld + c + e]) : 0.0f;
-        __nv_bfloat162 *d = reinterpret_cast<__nv_bfloat162 *>(dst + r * ldd + c);
-        for (int k = 0; k < parts; ++k) {
-            __nv_bfloat16 y[2];
-            for (int e = 0; e < 2; ++e) {
-                const bool fine = fabsf(x[e]) < kInf;
-                y[e] = __float2bfloat16_rn(x[e]);
-                if (fine && __hisinf(y[e])) y[e] = __float2bfloat16_rz(x[e]);
-                x[e] = fine ? x[e] - __bfloat162float(y[e]) : 0.0f;
+    const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (r >= rows) return;
+    const E *s = src + r * ld;
+    __nv_bfloat16 *d = dst + r * ldd;
+#pragma unroll 4
+    for (int c = threadIdx.x * N; c < ldd; c += 64 * N) {
+        alignas(16) E in[N];
+        if (N == 8 && c + N <= cols) {
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(in) / 16); ++i)
+                reinterpret_cast<uint4 *>(in)[i] = reinterpret_cast<const uint4 *>(s + c)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) in[i] = c + i < cols ? s[c + i] : static_cast<E>(0.0f);
+        }
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = static_cast<float>(in[i]);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            alignas(16) __nv_bfloat16 y[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                y[i] = __float2bfloat16_rn(x[i]);
+                if (PARTS > 1) {
+                    const bool fine = fabsf(x[i]) < kInf;
+                    if (fine && __hisinf(y[i])) y[i] = __float2bfloat16_rz(x[i]);
+                    x[i] = fine ? x[i] - __bfloat162float(y[i]) : 0.0f;
+                }
             }
-            *d = __nv_bfloat162(y[0], y[1]);
-            d += part / 2;
+            if constexpr (N == 8)
+                *reinterpret_cast<uint4 *>(d + k * part + c) = *reinterpret_cast<const uint4 *>(y);
+            else
+                *reinterpret_cast<uint32_t *>(d + k * part + c) = *reinterpret_cast<const uint32_t *>(y);
         }
     }
+}
+
+template <typename E, int PARTS>
+cudaError_t launch_parts(const E *src, long long ld, int rows, int cols, __nv_bfloat16 *dst, long long ldd,
+                         long long part, cudaStream_t stream)
+{
+    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld * sizeof(E) % 16 == 0;
+    const dim3 grid((rows + 3) / 4), block(64, 4);
+    if (vec)
+        vocab_parts_kernel<E, PARTS, 8><<<grid, block, 0, stream>>>(src, ld, rows, cols, dst, ldd, part);
+    else
+        vocab_parts_kernel<E, PARTS, 2><<<grid, block, 0, stream>>>(src, ld, rows, cols, dst, ldd, part);
+    return cudaGetLastError();
 }
 
 template <int CTAS>
@@ -734,8 +775,7 @@ int vocab_max_pairs()
 cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
                                const VocabTileParams &p, int ctas, int workers, cudaStream_t stream)
 {
-    const long long items = p.dh_items + p.dw_items + p.z_items;
-    const int n = static_cast<int>(std::min<long long>(items, workers));
+    const int n = static_cast<int>(std::min<long long>(static_cast<long long>(p.dh_items) + p.dw_items + p.z_items, workers));
     if (ctas == 2)
         return launch_kernel_cluster(false, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream, tmH,
                                      tmW, tmG, p);
@@ -743,18 +783,15 @@ cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, c
 }
 
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
-                               long long ldd, long long part, int num_sms, cudaStream_t stream)
+                               long long ldd, long long part, cudaStream_t stream)
 {
-    const long long blocks = (static_cast<long long>(rows) * (ldd / 2) + 1023) / 1024;
-    const int grid = static_cast<int>(std::min<long long>(std::max<long long>(blocks, 1), 16LL * num_sms));
     __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst);
     if (dtype == SGEMM_DTYPE_BF16)
-        vocab_parts_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, parts, d,
-                                                     ldd, part);
-    else
-        vocab_parts_kernel<<<grid, 256, 0, stream>>>(static_cast<const float *>(src), ld, rows, cols, parts, d, ldd,
-                                                     part);
-    return cudaGetLastError();
+        return launch_parts<__nv_bfloat16, 1>(static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, d, ldd, part,
+                                              stream);
+    const float *f = static_cast<const float *>(src);
+    return parts == 2 ? launch_parts<float, 2>(f, ld, rows, cols, d, ldd, part, stream)
+                      : launch_parts<float, 3>(f, ld, rows, cols, d, ldd, part, stream);
 }
 
 }  // namespace sgemm_impl

@@ -24,6 +24,11 @@ int validate_vocab(const VocabProblem &q)
     if (q.align_flags < 0 || q.align_flags > 3 || q.num_sms < 1) return SGEMM_ERR_INVALID_VALUE;
     if (q.math_mode != SGEMM_MATH_FP32 && q.math_mode != SGEMM_MATH_TF32) return SGEMM_ERR_INVALID_VALUE;
     if (q.n > SGEMM_DISTILL_MAX_ENTRIES) return SGEMM_ERR_NOT_SUPPORTED;
+    // tiles and coordinates are counted in 32 bits
+    const long long tiles_t = q.T / 128 + 1LL, tiles_v = q.V / 128 + 1LL, tiles_d = q.D / 128 + 1LL;
+    for (long long x : {tiles_t * tiles_v, tiles_t * tiles_d, tiles_v * tiles_d})
+        if (x > 1LL << 30) return SGEMM_ERR_NOT_SUPPORTED;
+    if (q.T > 0x7fff0000 || q.V > 0x7fff0000 || q.D > 0x7fff0000) return SGEMM_ERR_NOT_SUPPORTED;
     return SGEMM_OK;
 }
 
@@ -74,13 +79,15 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.g_off[0] = take(w.parts * T * w.ldg * 2);
         w.g_off[1] = w.pub.pieces > 1 ? take(w.parts * T * w.ldg * 2) : w.g_off[0];
         if (q.dh) {
-            // A dH tile's K range is a piece of the vocabulary, the other tiles' are T and D: it is split
-            // until its parts are about as long, and until there are two rounds of them, but not below 4 k-blocks.
+            // A dH tile's K range is a piece of the vocabulary, the other tiles' are T and D. It is split so far
+            // that no part of it takes a worker more than half its share of a launch (the other tiles fill what
+            // that leaves uneven), a quarter where there are no others; every split costs a pass over T x D sums.
             const int kblocks = (w.pub.piece + kVocabBK - 1) / kVocabBK;
-            const long long tiles = ((T + bm - 1) / bm) * ((q.D + kVocabBN - 1) / kVocabBN);
-            const long long even = (w.pub.piece + std::max<long long>({T, q.D, 1024}) - 1) / std::max<long long>({T, q.D, 1024});
-            const long long fill = tiles > 0 ? (2LL * w.workers + tiles - 1) / tiles : 1;
-            const long long s = std::min<long long>(std::max(even, fill), std::max(1, kblocks / 4));
+            const long long tm = (T + bm - 1) / bm, tn = (q.D + kVocabBN - 1) / kVocabBN;
+            const long long own = tm * tn * kblocks;
+            const long long others = q.dw ? (w.pub.piece + bm - 1) / bm * tn * vocab_cost(q.T) : 0;
+            const long long most = std::max<long long>(4, (own + others) / w.workers / (q.dw ? 2 : 4));
+            const long long s = std::max<long long>(1, (kblocks + most - 1) / most);
             w.dh_kb = static_cast<int>((kblocks + s - 1) / s);
             w.dh_splits = (kblocks + w.dh_kb - 1) / w.dh_kb;
             w.ldacc = round_up(q.D, 4);

@@ -66,10 +66,12 @@ vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const floa
     }
 }
 
-// 8 tokens per block, 32 lanes for each: lane l folds the (max, sum) pairs of tile
-// columns l, l + 32, ... (8 tokens' pairs are 64 contiguous bytes), then the lanes
-// fold theirs; a fixed order, so the result does not depend on scheduling.
-constexpr int kCombineRows = 8;
+// ROWS tokens per block, kCombineThreads / ROWS lanes for each: lane l folds the
+// (max, sum) pairs of columns l, l + lanes, ... (8 tokens' pairs are 64 contiguous
+// bytes), then a warp per token folds the lanes'; a fixed order, so the result does
+// not depend on scheduling. Latency decides: few tokens get fewer rows per block
+// and so more lanes each (60 tokens of 1024 pairs: 15.7 us with 32 lanes).
+constexpr int kCombineThreads = 512;
 
 __device__ __forceinline__ void fold(float &m, float &s, float m2, float s2)
 {
@@ -82,27 +84,34 @@ __device__ __forceinline__ void fold(float &m, float &s, float m2, float s2)
     m = top;
 }
 
-__global__ void __launch_bounds__(kCombineRows * 32)
+template <int ROWS>
+__global__ void __launch_bounds__(kCombineThreads)
 vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ part, int parts,
                      const float *__restrict__ zt, float mult, float *__restrict__ loss, float *__restrict__ lse)
 {
-    __shared__ float sm[32][kCombineRows + 1], ss[32][kCombineRows + 1];
-    const int r = threadIdx.x % kCombineRows, l = threadIdx.x / kCombineRows;
-    const long long first = static_cast<long long>(blockIdx.x) * kCombineRows;
+    constexpr int LANES = kCombineThreads / ROWS;
+    __shared__ float sm[LANES][ROWS + 1], ss[LANES][ROWS + 1];
+    const int r = threadIdx.x % ROWS, l = threadIdx.x / ROWS;
+    const long long first = static_cast<long long>(blockIdx.x) * ROWS;
     float m = -kInf, s = 0.0f;
-    if (first + r < T)
-        for (int c = l; c < parts; c += 32) {
-            const float2 x = part[static_cast<long long>(c) * T + first + r];
+    if (first + r < T) {
+        const float2 *row = part + first + r;
+#pragma unroll 4
+        for (int c = l; c < parts; c += LANES) {
+            const float2 x = row[static_cast<long long>(c) * T];
             fold(m, s, x.x, x.y);
         }
+    }
     sm[l][r] = m;
     ss[l][r] = s;
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // a warp per token
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= ROWS) return;  // a warp per token from here on
     const long long row = first + warp;
     if (row >= T) return;
-    m = sm[lane][warp];
-    s = ss[lane][warp];
+    m = -kInf;
+    s = 0.0f;
+    for (int i = lane; i < LANES; i += 32) fold(m, s, sm[i][warp], ss[i][warp]);
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
         const bool low = (lane & o) == 0;  // both lanes fold in the same order
@@ -130,20 +139,30 @@ vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ pa
     }
 }
 
-// The partial sums of a dH element in split order, then beta * dst, rounded once.
+// The partial sums of four neighbouring dH elements in split order, then beta * dst, rounded once. One
+// block per row and 1024 columns; reads at the memory's rate once there are a few rows (ldacc is a multiple of 4).
 template <typename E>
-__global__ void vocab_finish_kernel(int rows, int cols, const float *__restrict__ acc, long long ldacc, long long split,
-                                    int splits, float beta, E *__restrict__ dst, long long ldd)
+__global__ void __launch_bounds__(256)
+vocab_finish_kernel(int cols, const float *__restrict__ acc, long long ldacc, long long split, int splits, float beta,
+                    E *__restrict__ dst, long long ldd)
 {
-    const long long total = static_cast<long long>(rows) * cols;
-    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-        const long long r = i / cols, c = i % cols;
-        E *d = dst + r * ldd + c;
-        float x = 0.0f;
-        for (int s = 0; s < splits; ++s) x += acc[s * split + r * ldacc + c];
-        if (beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
-        *d = static_cast<E>(x);
+    const long long r = blockIdx.x;
+    const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (c >= cols) return;
+    float x[4] = {};
+    const float *a = acc + r * ldacc + c;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const float4 y = *reinterpret_cast<const float4 *>(a + s * split);
+        x[0] += y.x;
+        x[1] += y.y;
+        x[2] += y.z;
+        x[3] += y.w;
+    }
+    E *d = dst + r * ldd + c;
+    for (int e = 0; e < 4 && c + e < cols; ++e) {
+        if (beta != 0.0f) x[e] = fmaf(beta, static_cast<float>(d[e]), x[e]);
+        d[e] = static_cast<E>(x[e]);
     }
 }
 
@@ -159,22 +178,24 @@ cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, cons
 cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
                                  float mult, float *loss, float *lse, cudaStream_t stream)
 {
-    vocab_combine_kernel<<<(T + kCombineRows - 1) / kCombineRows, kCombineRows * 32, 0, stream>>>(
-        T, V, t, part, parts, zt, mult, loss, lse);
+    // eight rows per block read whole sectors; below four blocks of them per SM more lanes per row are worth more
+    if (T > 4096)
+        vocab_combine_kernel<8><<<(T + 7) / 8, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
+    else
+        vocab_combine_kernel<2><<<(T + 1) / 2, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
     return cudaGetLastError();
 }
 
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
-                                float beta, void *dst, long long ldd, int dtype, int num_sms, cudaStream_t stream)
+                                float beta, void *dst, long long ldd, int dtype, cudaStream_t stream)
 {
-    const long long blocks = (static_cast<long long>(rows) * cols + 1023) / 1024;
-    const int grid = static_cast<int>(std::min<long long>(std::max<long long>(blocks, 1), 8LL * num_sms));
+    const dim3 grid(rows, (cols + 1023) / 1024);
     if (dtype == SGEMM_DTYPE_BF16)
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, split, splits, beta,
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(cols, acc, ldacc, split, splits, beta,
                                                       static_cast<__nv_bfloat16 *>(dst), ldd);
     else
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(rows, cols, acc, ldacc, split, splits, beta,
-                                                      static_cast<float *>(dst), ldd);
+        vocab_finish_kernel<<<grid, 256, 0, stream>>>(cols, acc, ldacc, split, splits, beta, static_cast<float *>(dst),
+                                                      ldd);
     return cudaGetLastError();
 }
 
