@@ -73,17 +73,20 @@ int check(const Call &c, bool grad)
     return SGEMM_OK;
 }
 
-// Map of a (rows x cols) bfloat16 matrix of `parts` parts, in boxes of 64 x 64.
-int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int cols, int rows, long long ld, int parts,
-             long long part)
+// Map of a (rows x cols) matrix of `parts` parts: operands are read in boxes of 64 x 64, results written in boxes of
+// 128 bytes x 32 rows.
+int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int dtype, int cols, int rows, long long ld, int parts,
+             long long part, bool result)
 {
+    const cuuint64_t size = dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2u, static_cast<cuuint64_t>(part) * 2u};
-    cuuint32_t box[3] = {64, 64, 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size, static_cast<cuuint64_t>(part) * size};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), result ? 32u : 64u, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = h->encode(map, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                                 const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
@@ -91,23 +94,23 @@ int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int cols, int
 int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src, int rows, int ld, long long off,
                 long long ldp, CUtensorMap *map)
 {
-    if (!copy) {
-        return make_map(c.h, map, src, c.D, rows, ld, 1, static_cast<long long>(ld) * rows);
-    }
+    if (!copy)
+        return make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
     void *dst = static_cast<char *>(c.h->workspace) + off;
     const long long part = rows * ldp;
     if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
-    return make_map(c.h, map, dst, c.D, rows, ldp, w.parts, part);
+    return make_map(c.h, map, dst, SGEMM_DTYPE_BF16, c.D, rows, ldp, w.parts, part, false);
 }
 
 // Operands, targets (the distillation's tables are made first) and what every launch of the call shares.
-int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, CUtensorMap *tmH, CUtensorMap *tmW)
+int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
 {
     char *ws = static_cast<char *>(c.h->workspace);
     int rc;
-    if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, tmH)) != SGEMM_OK) return rc;
-    if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, tmW)) != SGEMM_OK) return rc;
+    if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, &m->H)) != SGEMM_OK) return rc;
+    if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, &m->W)) != SGEMM_OK) return rc;
+    m->G = m->Gw = m->acc = m->dW = m->W;  // where a call has no such matrix, a valid map that no tile uses
     p->T = c.T;
     p->V = c.V;
     p->D = c.D;
@@ -120,7 +123,6 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, CUtensorMap *
     p->scale = c.scale;
     p->lse = c.lse;
     p->dloss = c.dloss;
-    p->gmult = c.mult * c.scale;
     p->status = c.h->d_status;
     p->timeout_ns = c.h->timeout_ns;
     p->t.labels = c.labels;
@@ -150,15 +152,15 @@ int run_loss(const Call &c)
     if ((rc = ensure_workspace(c.h, static_cast<size_t>(w.pub.workspace_bytes), c.stream)) != SGEMM_OK) return rc;
     char *ws = static_cast<char *>(c.h->workspace);
     VocabTileParams p{};
-    CUtensorMap tmH, tmW;
-    if ((rc = begin(c, w, &p, &tmH, &tmW)) != SGEMM_OK) return rc;
+    VocabMaps m;
+    if ((rc = begin(c, w, &p, &m)) != SGEMM_OK) return rc;
     p.z_kind = kVocabLoss;
     p.z_tm = ceil_div(c.T, 128 * w.ctas);
     p.z_tn = ceil_div(c.V, kVocabBN);
     p.z_items = p.z_tm * p.z_tn;
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
-    if (launch_vocab_tiles(tmH, tmW, tmW, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     if (launch_vocab_combine(c.T, c.V, p.t, p.part, w.stat_cols, p.zt, c.mult, c.loss, c.lse_out, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;
@@ -181,28 +183,34 @@ int run_grad(const Call &c)
     if ((rc = ensure_workspace(c.h, static_cast<size_t>(w.pub.workspace_bytes), c.stream)) != SGEMM_OK) return rc;
     char *ws = static_cast<char *>(c.h->workspace);
     VocabTileParams p{};
-    CUtensorMap tmH, tmW;
-    if ((rc = begin(c, w, &p, &tmH, &tmW)) != SGEMM_OK) return rc;
+    VocabMaps m;
+    if ((rc = begin(c, w, &p, &m)) != SGEMM_OK) return rc;
     const int bm = 128 * w.ctas, tm = ceil_div(c.T, bm), tn = ceil_div(c.D, kVocabBN);
     const int elem = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     p.z_kind = kVocabDz;
     p.z_tm = tm;
     p.ldg = w.ldg;
-    p.g_part = c.T * w.ldg;
+    const long long g_part = c.T * w.ldg, acc_split = c.T * w.ldacc;
+    float *acc = reinterpret_cast<float *>(ws + w.acc_off);
     p.dW = c.dW;
     p.lddw = c.lddw;
+    p.dw_tma = c.beta == 0.0f && aligned(c.dW, 16) && static_cast<long long>(c.lddw) * elem % 16 == 0;
     p.dw_vec = aligned(c.dW, 4 * elem) && c.lddw % 4 == 0;
+    p.alpha = c.mult * c.scale;
     p.beta = c.beta;
     p.dw_tn = tn;
     p.dh_tm = tm;
     p.dh_tn = tn;
     p.dh_kb = w.dh_kb;
-    p.acc = reinterpret_cast<float *>(ws + w.acc_off);
-    p.ldacc = w.ldacc;
-    p.acc_split = c.T * w.ldacc;
+    if (c.dW != nullptr && p.dw_tma &&
+        (rc = make_map(c.h, &m.dW, c.dW, c.dtype, c.D, c.V, c.lddw, 1, static_cast<long long>(c.lddw) * c.V, true)) !=
+            SGEMM_OK)
+        return rc;
+    if (c.dH != nullptr && (rc = make_map(c.h, &m.acc, acc, SGEMM_DTYPE_F32, c.D, c.T, w.ldacc, w.dh_splits, acc_split,
+                                          true)) != SGEMM_OK)
+        return rc;
     // Launch i: the dH and dW tiles of piece i - 1 and the dZ tiles of piece i.
     for (int i = 0; i <= w.pub.pieces; ++i) {
-        CUtensorMap tmG = tmW;
         p.dh_items = p.dw_items = p.z_items = 0;
         if (i > 0) {
             p.g_v0 = (i - 1) * w.pub.piece;
@@ -211,21 +219,25 @@ int run_grad(const Call &c)
             if (c.dH != nullptr) p.dh_items = tm * tn * splits;
             if (c.dW != nullptr) p.dw_items = ceil_div(p.g_vn, bm) * tn;
             p.acc_add = i > 1;
-            if ((rc = make_map(c.h, &tmG, ws + w.g_off[(i - 1) & 1], p.g_vn, c.T, w.ldg, w.parts, p.g_part)) != SGEMM_OK)
+            // only the piece's own columns: the product's K range ends with them
+            if ((rc = make_map(c.h, &m.G, ws + w.g_off[(i - 1) & 1], SGEMM_DTYPE_BF16, p.g_vn, c.T, w.ldg, w.parts, g_part,
+                               false)) != SGEMM_OK)
                 return rc;
         }
         if (i < w.pub.pieces) {
             p.z_v0 = i * w.pub.piece;
             p.z_tn = ceil_div(c.V - p.z_v0 < w.pub.piece ? c.V - p.z_v0 : w.pub.piece, kVocabBN);
             p.z_items = tm * p.z_tn;
-            p.Gw = reinterpret_cast<__nv_bfloat16 *>(ws + w.g_off[i & 1]);
+            if ((rc = make_map(c.h, &m.Gw, ws + w.g_off[i & 1], SGEMM_DTYPE_BF16, static_cast<int>(w.ldg), c.T, w.ldg,
+                               w.parts, g_part, true)) != SGEMM_OK)
+                return rc;
         }
         const int others = p.dw_items + p.z_items, rem = p.dh_items % w.workers;
         const int cost = vocab_cost(c.dW != nullptr ? c.T : c.D);
         p.dh_extra = p.dh_items > 0 && rem > 0 ? std::min((w.dh_kb + cost / 2) / cost, others / (w.workers - rem)) : 0;
-        if (launch_vocab_tiles(tmH, tmW, tmG, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
-    if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, p.acc, w.ldacc, p.acc_split, w.dh_splits, c.beta, c.dH, c.lddh,
+    if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, acc, w.ldacc, acc_split, w.dh_splits, c.beta, c.dH, c.lddh,
                                                c.dtype, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;

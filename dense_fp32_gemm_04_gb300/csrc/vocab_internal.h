@@ -90,31 +90,31 @@ struct VocabTileParams {
     float2 *part;
     float *zt;
     const float *lse, *dloss;
-    float gmult;         // c * scale
-    __nv_bfloat16 *Gw;   // dZ written
-    long long ldg, g_part;  // row stride, elements between parts
+    long long ldg;       // columns of dZ's buffer
     // dH and dW tiles of the piece [g_v0, g_v0 + g_vn), whose dZ an earlier launch left
     int g_v0, g_vn;
     int dw_tn;
     int dw_items;
     void *dW;
     long long lddw;
-    bool dw_vec;  // rows of dW can be written 4 elements at a time
-    float beta;
+    bool dw_tma, dw_vec;  // dW is written by TMA stores; else whether 4 elements of a row at a time
+    float alpha, beta;    // dH = alpha * G W (summed over the pieces), dW = alpha * G^T H + beta * dW, alpha = c * scale
     int dh_tm, dh_tn, dh_kb;
     int dh_items;
     int dh_extra;  // other tiles for a worker that has one dH tile fewer
-    float *acc;
-    long long ldacc, acc_split;
-    bool acc_add;  // add to the sums (a later piece)
+    bool acc_add;  // dH: add to the sums (a later piece)
     int *status;
     long long timeout_ns;
 };
 cudaError_t vocab_set_attributes();
 int vocab_max_pairs();
-// Maps of H, W and the piece's dZ: (elements of a row, rows, parts), boxes of 64 x 64 x 1, 128-byte swizzle.
-cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
-                               const VocabTileParams &p, int ctas, int workers, cudaStream_t stream);
+// Maps (elements of a row, rows, parts), all with the 128-byte swizzle: operands in boxes of 64 x 64 x 1 (H, W, the
+// piece's dZ G), results in boxes of 128 bytes x 32 rows (dZ written, the sums of dH by split, dW where dw_tma).
+struct VocabMaps {
+    CUtensorMap H, W, G, Gw, acc, dW;
+};
+cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers,
+                               cudaStream_t stream);
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
                                long long ldd, long long part, cudaStream_t stream);
 

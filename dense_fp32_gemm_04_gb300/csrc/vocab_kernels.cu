@@ -58,8 +58,7 @@ constexpr int REGS_LAUNCH = 168, REGS_ISSUE = 72, REGS_EPILOGUE = 216;
 static_assert(REGS_ISSUE + 2 * REGS_EPILOGUE <= 3 * REGS_LAUNCH, "an exchange above the launch's registers never ends");
 constexpr int COLS = 128;      // accumulator columns of one epilogue thread
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int kPitch = 33;     // floats between staged rows: row- and column-wise accesses without bank conflicts
-constexpr int kStagingBytes = EPI_WARPS * 32 * kPitch * 4;
+constexpr int kWarpStaging = 32 * 128;  // bytes: 32 rows of 128 (64 bfloat16 or 32 floats)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -71,7 +70,7 @@ struct Shape {
     static constexpr int A_BYTES = 128 * BK * 2;
     static constexpr int B_BYTES = CTA_N * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 512 + kStagingBytes;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * kWarpStaging + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -169,76 +168,137 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-// The thread's 128 columns of one row, written where they belong through the
-// warp's staging area, so that the stores of a warp run along rows: 32 columns at
-// a time, thread l's row into staged row l, then 8 lanes per row (16-byte rows) or
-// 32 lanes along one row (any alignment).
-enum { kToUser, kToAcc, kAddToAcc };
+// A warp's 32 rows x 128 columns leave through its staging area: rows of 128 bytes
+// with the 128-byte swizzle (16-byte chunk j of row r at j ^ (r & 7)), so that each
+// lane writes its own row without bank conflicts and one TMA store (or addition)
+// per 128 bytes of columns takes them out in the background, clipped to the map.
 
-template <int MODE, typename E>
-__device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg, int lane, E *dst, long long ld, int rows,
-                                           int cols, bool vec, float beta)
+// Take the staging area back from the copies that still read it.
+__device__ __forceinline__ void stage_free(int lane)
+{
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
+}
+
+// The staged block to columns x.., rows y.. of part z.
+__device__ __forceinline__ void stage_send(const CUtensorMap *map, uint32_t stg, int lane, int x, int y, int z, bool add)
+{
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+        if (add)
+            tma_add_3d(map, stg, x, y, z);
+        else
+            tma_store_3d(map, stg, x, y, z);
+        bulk_commit();
+    }
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4])
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+// alpha * FP32 columns, 32 per block. (Scaling here and not in dZ also lets the stores' groups of four registers be
+// others than the accumulator's: without it the kernel spills 60 of them.)
+__device__ __forceinline__ void send_f32(const CUtensorMap *map, const float (&acc)[COLS], uint32_t stg, int lane, int x,
+                                         int y, int z, int cols, bool add, float alpha)
 {
 #pragma unroll
     for (int cb = 0; cb < COLS / 32; ++cb) {
+        if (x + cb * 32 >= cols) break;
+        stage_free(lane);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) stg[lane * kPitch + i] = acc[cb * 32 + i];
-        __syncwarp();
-        if (cb * 32 < cols) {
-            if (vec) {
-                const int sub = lane >> 3, c = cb * 32 + 4 * (lane & 7);
+        for (int j = 0; j < 8; ++j) {
+            const float *f = acc + cb * 32 + 4 * j;
+            const uint32_t v[4] = {__float_as_uint(alpha * f[0]), __float_as_uint(alpha * f[1]),
+                                   __float_as_uint(alpha * f[2]), __float_as_uint(alpha * f[3])};
+            sts128(stg + lane * 128 + ((j ^ (lane & 7)) << 4), v);
+        }
+        stage_send(map, stg, lane, x + cb * 32, y, z, add);
+    }
+}
+
+// alpha * columns as bfloat16, 64 per block, in parts: each but the last leaves its remainder (exact in FP32) to the next.
+__device__ __forceinline__ void send_bf16(const CUtensorMap *map, float (&acc)[COLS], uint32_t stg, int lane, int x,
+                                          int y, int cols, int parts, float alpha)
+{
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = 4 * k + sub;
-                    const float *s = stg + r * kPitch + 4 * (lane & 7);
-                    float x[4] = {s[0], s[1], s[2], s[3]};
-                    if (r >= rows || c >= cols) continue;
-                    E *d = dst + r * ld + c;
-                    if (c + 3 < cols) {
-                        if constexpr (MODE == kAddToAcc) {
-                            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(d), "f"(x[0]), "f"(x[1]),
-                                         "f"(x[2]), "f"(x[3])
-                                         : "memory");
-                        } else if constexpr (sizeof(E) == 4) {
-                            if (MODE == kToUser && beta != 0.0f) {
-                                const float4 o = *reinterpret_cast<const float4 *>(d);
-                                x[0] = fmaf(beta, o.x, x[0]);
-                                x[1] = fmaf(beta, o.y, x[1]);
-                                x[2] = fmaf(beta, o.z, x[2]);
-                                x[3] = fmaf(beta, o.w, x[3]);
-                            }
-                            *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
-                        } else {
-                            __nv_bfloat162 *d2 = reinterpret_cast<__nv_bfloat162 *>(d);
-                            if (beta != 0.0f) {
-                                const float2 o0 = __bfloat1622float2(d2[0]), o1 = __bfloat1622float2(d2[1]);
-                                x[0] = fmaf(beta, o0.x, x[0]);
-                                x[1] = fmaf(beta, o0.y, x[1]);
-                                x[2] = fmaf(beta, o1.x, x[2]);
-                                x[3] = fmaf(beta, o1.y, x[3]);
-                            }
-                            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
-                            *reinterpret_cast<uint2 *>(d) = *reinterpret_cast<const uint2 *>(y);
-                        }
-                    } else {
-                        for (int e = 0; e < 4; ++e)
-                            if (c + e < cols) {
-                                if (MODE == kAddToAcc || (MODE == kToUser && beta != 0.0f))
-                                    x[e] = fmaf(MODE == kAddToAcc ? 1.0f : beta, static_cast<float>(d[e]), x[e]);
-                                d[e] = static_cast<E>(x[e]);
-                            }
-                    }
+    for (int cb = 0; cb < COLS / 64; ++cb) {
+        if (x + cb * 64 >= cols) break;
+        for (int part = 0;;) {
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float *f = acc + cb * 64 + 8 * j + 2 * i;
+                    const __nv_bfloat162 y2 = __floats2bfloat162_rn(alpha * f[0], alpha * f[1]);
+                    v[i] = *reinterpret_cast<const uint32_t *>(&y2);
                 }
-            } else {
-                const int c = cb * 32 + lane;
-#pragma unroll 4
-                for (int r = 0; r < 32; ++r) {
-                    float x = stg[r * kPitch + lane];
-                    if (r < rows && c < cols) {
-                        E *d = dst + r * ld + c;
-                        if (MODE == kToUser && beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
-                        *d = static_cast<E>(x);
+                sts128(stg + lane * 128 + ((j ^ (lane & 7)) << 4), v);
+            }
+            stage_send(map, stg, lane, x + cb * 64, y, part, false);
+            if (++part == parts) break;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {  // (more than one part: dZ, whose alpha is 1)
+                float &f = acc[cb * 64 + i];
+                f -= __bfloat162float(__float2bfloat16_rn(f));
+            }
+        }
+    }
+}
+
+// Rows that a TMA store cannot write (not 16-byte aligned), or that are added to (beta != 0), element by element or
+// four at a time: 32 columns of FP32 staged, element (r, c) at 32 r + (c ^ r), then read back along rows.
+template <typename E>
+__device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg, int lane, E *dst, long long ld, int rows,
+                                           int cols, bool vec, float alpha, float beta)
+{
+#pragma unroll
+    for (int cb = 0; cb < COLS / 32; ++cb) {
+        stage_free(lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stg[lane * 32 + (i ^ lane)] = alpha * acc[cb * 32 + i];
+        __syncwarp();
+        if (vec) {  // 8 lanes per row
+            const int sub = lane >> 3, c = 4 * (lane & 7);
+            for (int k = 0; k < 8; ++k) {
+                const int r = 4 * k + sub;
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = stg[r * 32 + ((c + e) ^ r)];
+                if (r >= rows || cb * 32 + c >= cols) continue;
+                E *d = dst + r * ld + cb * 32 + c;
+                if (cb * 32 + c + 3 < cols) {
+                    if constexpr (sizeof(E) == 4) {
+                        float4 y = beta != 0.0f ? *reinterpret_cast<const float4 *>(d) : make_float4(0, 0, 0, 0);
+                        *reinterpret_cast<float4 *>(d) = make_float4(fmaf(beta, y.x, x[0]), fmaf(beta, y.y, x[1]),
+                                                                     fmaf(beta, y.z, x[2]), fmaf(beta, y.w, x[3]));
+                    } else {
+                        __nv_bfloat162 *d2 = reinterpret_cast<__nv_bfloat162 *>(d);
+                        const float2 y0 = beta != 0.0f ? __bfloat1622float2(d2[0]) : make_float2(0, 0);
+                        const float2 y1 = beta != 0.0f ? __bfloat1622float2(d2[1]) : make_float2(0, 0);
+                        d2[0] = __floats2bfloat162_rn(fmaf(beta, y0.x, x[0]), fmaf(beta, y0.y, x[1]));
+                        d2[1] = __floats2bfloat162_rn(fmaf(beta, y1.x, x[2]), fmaf(beta, y1.y, x[3]));
                     }
+                } else {
+                    for (int e = 0; e < 4; ++e)
+                        if (cb * 32 + c + e < cols)
+                            d[e] = static_cast<E>(beta != 0.0f ? fmaf(beta, static_cast<float>(d[e]), x[e]) : x[e]);
+                }
+            }
+        } else {  // 32 lanes along one row
+            const int c = cb * 32 + lane;
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r) {
+                float x = stg[r * 32 + (lane ^ r)];
+                if (r < rows && c < cols) {
+                    E *d = dst + r * ld + c;
+                    if (beta != 0.0f) x = fmaf(beta, static_cast<float>(*d), x);
+                    *d = static_cast<E>(x);
                 }
             }
         }
@@ -302,64 +362,35 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     });
 }
 
-// Z tile of a gradient call: dZ = g (exp(z - lse) - q), in bfloat16 parts. The last part is rounded to
-// nearest, as the earlier ones are: their remainders are exact in FP32.
-template <int PARTS>
-__device__ __forceinline__ void store_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c)
+// Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q). Rows past T and columns past
+// the vocabulary hold what no copy of the products reads.
+__device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
 {
-    __nv_bfloat16 *dst = p.Gw + row * p.ldg + c;
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-#pragma unroll
-        for (int i = 0; i < COLS; i += 8) {
-            __nv_bfloat162 y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = __floats2bfloat162_rn(z[i + 2 * j], z[i + 2 * j + 1]);
-                if (part + 1 < PARTS) {
-                    const float2 back = __bfloat1622float2(y[j]);
-                    z[i + 2 * j] -= back.x;
-                    z[i + 2 * j + 1] -= back.y;
-                }
-            }
-            *reinterpret_cast<uint4 *>(dst + i) = *reinterpret_cast<const uint4 *>(y);
-        }
-        dst += p.g_part;
+    const bool live = row < p.T;
+    bool used = false;
+    float g = 0.0f, l = 0.0f;
+    if (live) {
+        const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
+        used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
+        if (used) g = p.dloss[row];
+        l = p.lse[row];
     }
-}
-
-__device__ __forceinline__ void leave_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
-{
-    if (row >= p.T) return;
-    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
-    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
-    const float g = used ? p.gmult * p.dloss[row] : 0.0f, l = p.lse[row];
 #pragma unroll
     for (int i = 0; i < COLS; ++i) {
         const float e = g * exp2_approx((z[i] * p.scale - l) * kLog2e);
         z[i] = used ? e : 0.0f;  // a masked token's dZ is 0 whatever its logits are
     }
-    for_targets(p, row, true, c0, [&](int at, int, float q) {
+    for_targets(p, row, live, c0, [&](int at, int, float q) {
         const float t = g * q;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) z[i] -= i == at ? t : 0.0f;
     });
-    // ldg covers whole tiles; columns past the vocabulary hold what the products' copies never read
-    const int c = c0 - p.z_v0;
-    if (!index_ok(c >= 0 && c + COLS <= p.ldg, p.status, kWhereIdxVocabDz)) return;
-    if (p.parts == 1)
-        store_dz<1>(p, z, row, c);
-    else if (p.parts == 2)
-        store_dz<2>(p, z, row, c);
-    else
-        store_dz<3>(p, z, row, c);
 }
 
 // Producer thread: this CTA's part of each stage, in boxes of 64 rows x 64 elements.
 template <int CTAS>
 __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, uint32_t a_base,
-                                        uint32_t b_base, const CUtensorMap &tmH, const CUtensorMap &tmW,
-                                        const CUtensorMap &tmG, uint32_t rank, int worker, int workers)
+                                        uint32_t b_base, const VocabMaps &maps, uint32_t rank, int worker, int workers)
 {
     using S = Shape<CTAS>;
     constexpr int STAGES = S::STAGES;
@@ -371,8 +402,8 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
     Item w;
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool z = w.kind == kVocabLoss || w.kind == kVocabDz;
-        const CUtensorMap *ta = z ? &tmH : &tmG;
-        const CUtensorMap *tb = w.kind == kVocabDw ? &tmH : &tmW;
+        const CUtensorMap *ta = z ? &maps.H : &maps.G;
+        const CUtensorMap *tb = w.kind == kVocabDw ? &maps.H : &maps.W;
         const bool a_k = w.kind != kVocabDw, b_k = z;  // K-major: K along the map's rows
         const int a_r = w.m0 + static_cast<int>(rank) * 128;
         const int b_r = w.n0 + static_cast<int>(rank) * S::CTA_N + (z ? p.z_v0 : 0);
@@ -513,14 +544,16 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
 
 // Epilogue warp: the segments of a tile added up in registers, then the tile left as its kind wants it.
 template <int CTAS>
-__device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, float *staging,
-                                            uint32_t tmem, uint32_t rank, int warp, int lane, int worker, int workers)
+__device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars,
+                                            unsigned char *staging, const VocabMaps &maps, uint32_t tmem, uint32_t rank,
+                                            int warp, int lane, int worker, int workers)
 {
     using S = Shape<CTAS>;
     constexpr bool PAIR = CTAS == 2;
     volatile int *abort_flag = &bars->abort_flag;
     const int quarter = warp & 3, half = warp >> 3;
-    float *stg = staging + (warp - 4) * 32 * kPitch;
+    unsigned char *area = staging + (warp - 4) * kWarpStaging;
+    const uint32_t stg = smem_addr(area);
     int it = 0;
     bool ok = true;
     Item w;
@@ -562,31 +595,46 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         const int c0 = w.n0 + half * COLS;
         if (w.kind == kVocabLoss) {
             leave_loss(p, acc, r0 + lane, p.z_v0 + c0);
-        } else if (w.kind == kVocabDz) {
-            leave_dz(p, acc, r0 + lane, p.z_v0 + c0);
-        } else if (w.kind == kVocabDw) {
-            const int rows = p.g_vn - r0, cols = p.D - c0;
-            const long long at = static_cast<long long>(p.g_v0 + r0) * p.lddw + c0;
-            if (p.dtype == SGEMM_DTYPE_BF16)
-                write_rows<kToUser>(acc, stg, lane, static_cast<__nv_bfloat16 *>(p.dW) + at, p.lddw, rows, cols,
-                                    p.dw_vec, p.beta);
-            else
-                write_rows<kToUser>(acc, stg, lane, static_cast<float *>(p.dW) + at, p.lddw, rows, cols, p.dw_vec,
-                                    p.beta);
+            continue;
+        }
+        // the rest are rows of a matrix: rows from `row` and columns from c0 of the map, as FP32 or in bfloat16 parts
+        const CUtensorMap *map = &maps.dW;
+        const bool wide = w.kind == kVocabDh || (w.kind == kVocabDw && p.dtype == SGEMM_DTYPE_F32);
+        int row = r0, cols = p.D, parts = 1;
+        bool inside = r0 < p.T;
+        if (w.kind == kVocabDz) {
+            make_dz(p, acc, r0 + lane, p.z_v0 + c0);
+            map = &maps.Gw;
+            cols = static_cast<int>(p.ldg);
+            parts = p.parts;
+            inside = inside && index_ok(c0 + COLS <= p.ldg, p.status, kWhereIdxVocabDz);
+        } else if (w.kind == kVocabDh) {
+            map = &maps.acc;
         } else {
-            float *dst = p.acc + w.split * p.acc_split + static_cast<long long>(r0) * p.ldacc + c0;
-            if (p.acc_add)
-                write_rows<kAddToAcc>(acc, stg, lane, dst, p.ldacc, p.T - r0, p.D - c0, true, 0.0f);
+            row = p.g_v0 + r0;
+            inside = r0 < p.g_vn;
+        }
+        if (!inside) continue;
+        if (w.kind == kVocabDw && !p.dw_tma) {
+            const long long at = static_cast<long long>(row) * p.lddw + c0;
+            if (wide)
+                write_rows(acc, reinterpret_cast<float *>(area), lane, static_cast<float *>(p.dW) + at, p.lddw,
+                           p.g_vn - r0, p.D - c0, p.dw_vec, p.alpha, p.beta);
             else
-                write_rows<kToAcc>(acc, stg, lane, dst, p.ldacc, p.T - r0, p.D - c0, true, 0.0f);
+                write_rows(acc, reinterpret_cast<float *>(area), lane, static_cast<__nv_bfloat16 *>(p.dW) + at, p.lddw,
+                           p.g_vn - r0, p.D - c0, p.dw_vec, p.alpha, p.beta);
+        } else if (wide) {
+            send_f32(map, acc, stg, lane, c0, row, w.split, cols, w.kind == kVocabDh && p.acc_add, p.alpha);
+        } else {
+            send_bf16(map, acc, stg, lane, c0, row, cols, parts, w.kind == kVocabDz ? 1.0f : p.alpha);
         }
     }
+    if (lane == 0) bulk_wait();  // the staging area is read and everything is written before the CTA ends
 }
 
 template <int CTAS>
 __global__ void __launch_bounds__(THREADS, 1)
-vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
-             const __grid_constant__ CUtensorMap tmG, const __grid_constant__ VocabTileParams p)
+vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabTileParams p)
 {
     using S = Shape<CTAS>;
     constexpr int STAGES = S::STAGES;
@@ -596,8 +644,8 @@ vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CU
     unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t a_base = smem_addr(smem);
     const uint32_t b_base = a_base + STAGES * S::A_BYTES;
-    Bars<STAGES> *bars = reinterpret_cast<Bars<STAGES> *>(smem + STAGES * S::STAGE_BYTES);
-    float *staging = reinterpret_cast<float *>(smem + STAGES * S::STAGE_BYTES + 512);
+    unsigned char *staging = smem + STAGES * S::STAGE_BYTES;
+    Bars<STAGES> *bars = reinterpret_cast<Bars<STAGES> *>(staging + EPI_WARPS * kWarpStaging);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (PAIR && cluster_size() != 2) {
@@ -622,9 +670,9 @@ vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CU
         bars->abort_flag = 0;
         bars->ring_offset = a_base;
         fence_barrier_init();
-        prefetch_tensormap(&tmH);
-        prefetch_tensormap(&tmW);
-        prefetch_tensormap(&tmG);
+        prefetch_tensormap(&maps.H);
+        prefetch_tensormap(&maps.W);
+        prefetch_tensormap(&maps.G);
     }
     if (warp == 0) {
         if constexpr (PAIR) {
@@ -652,12 +700,12 @@ vocab_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CU
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
         if (same_layout && warp == 0 && lane == 0)
-            produce<CTAS>(p, bars, a_base, b_base, tmH, tmW, tmG, rank, worker, workers);
+            produce<CTAS>(p, bars, a_base, b_base, maps, rank, worker, workers);
         else if (same_layout && warp == 1 && lane == 0 && rank == 0)
             issue<CTAS>(p, bars, a_base, b_base, tmem, worker, workers);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPILOGUE));
-        if (same_layout) leave_tiles<CTAS>(p, bars, staging, tmem, rank, warp, lane, worker, workers);
+        if (same_layout) leave_tiles<CTAS>(p, bars, staging, maps, tmem, rank, warp, lane, worker, workers);
     }
 
     tc_fence_before_sync();
@@ -772,14 +820,14 @@ int vocab_max_pairs()
     return clusters;
 }
 
-cudaError_t launch_vocab_tiles(const CUtensorMap &tmH, const CUtensorMap &tmW, const CUtensorMap &tmG,
-                               const VocabTileParams &p, int ctas, int workers, cudaStream_t stream)
+cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers,
+                               cudaStream_t stream)
 {
     const int n = static_cast<int>(std::min<long long>(static_cast<long long>(p.dh_items) + p.dw_items + p.z_items, workers));
     if (ctas == 2)
-        return launch_kernel_cluster(false, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream, tmH,
-                                     tmW, tmG, p);
-    return launch_kernel(false, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, tmH, tmW, tmG, p);
+        return launch_kernel_cluster(false, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream,
+                                     maps, p);
+    return launch_kernel(false, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, maps, p);
 }
 
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,

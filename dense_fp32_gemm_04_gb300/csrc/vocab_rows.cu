@@ -178,8 +178,8 @@ cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, cons
 cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
                                  float mult, float *loss, float *lse, cudaStream_t stream)
 {
-    // eight rows per block read whole sectors; below four blocks of them per SM more lanes per row are worth more
-    if (T > 4096)
+    // eight rows per block read whole sectors; below a block of them per SM more lanes per row are worth more
+    if (T > 1024)
         vocab_combine_kernel<8><<<(T + 7) / 8, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
     else
         vocab_combine_kernel<2><<<(T + 1) / 2, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
