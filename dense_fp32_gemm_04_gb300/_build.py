@@ -24,8 +24,8 @@ OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 DEBUG_LIB = os.path.join(OUT_DIR, "libsgemm_gb300_debug.so")
 DEBUG_OBJ_DIR = os.path.join(ROOT, "_build", "obj_debug")
 
-SOURCES = ["ffma_kernels.cu", "tf32_kernels.cu", "min2_kernels.cu", "ladder_kernels.cu", "vocab_kernels.cu", "vocab_rows.cu",
-           "planner.cpp", "vocab_plan.cpp", "sgemm_api.cpp", "vocab_api.cpp", "static_scratch.cu"]
+SOURCES = ["ffma_kernels.cu", "tf32_kernels.cu", "min2_kernels.cu", "ladder_kernels.cu", "vocab_kernels.cu", "vocab_few.cu",
+           "vocab_rows.cu", "planner.cpp", "vocab_plan.cpp", "sgemm_api.cpp", "vocab_api.cpp", "static_scratch.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -107,10 +107,12 @@ int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src,
 int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
 {
     char *ws = static_cast<char *>(c.h->workspace);
-    int rc;
-    if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, &m->H)) != SGEMM_OK) return rc;
-    if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, &m->W)) != SGEMM_OK) return rc;
-    m->G = m->Gw = m->acc = m->dW = m->W;  // where a call has no such matrix, a valid map that no tile uses
+    if (!w.few) {
+        int rc;
+        if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, &m->H)) != SGEMM_OK) return rc;
+        if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, &m->W)) != SGEMM_OK) return rc;
+        m->G = m->Gw = m->acc = m->dW = m->W;  // where a call has no such matrix, a valid map that no tile uses
+    }
     p->T = c.T;
     p->V = c.V;
     p->D = c.D;
@@ -160,7 +162,14 @@ int run_loss(const Call &c)
     p.z_items = p.z_tm * p.z_tn;
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
-    if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    if (w.few) {
+        const VocabFewParams f{c.T, c.V, c.D, static_cast<const float *>(c.H), static_cast<const float *>(c.W), c.ldh,
+                               c.ldw, c.scale, p.t, p.part, p.zt, 0};
+        const bool vec = problem(c).align_flags == 3;
+        if (launch_vocab_few(f, vec, c.h->num_sms, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) {
+        return SGEMM_ERR_LAUNCH;
+    }
     if (launch_vocab_combine(c.T, c.V, p.t, p.part, w.stat_cols, p.zt, c.mult, c.loss, c.lse_out, c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;

@@ -44,6 +44,7 @@ struct VocabProblem {
 // What a call does, and the byte offsets of the parts of its workspace (those a call does not use are empty).
 struct VocabLayout {
     sgemm_vocab_plan_t pub;
+    bool few;      // a few FP32 tokens: vocab_few.cu, no parts
     int ctas;      // CTAs per worker: 2 = pairs computing 256 x 256 tiles, 1 = 128 x 256
     int workers;
     int parts, products;  // bfloat16 parts of an operand, products of parts
@@ -51,8 +52,8 @@ struct VocabLayout {
     long long h_off, ldh, w_off, ldw;      // bytes, elements
     long long tid_off, tq_off, tlogq_off;  // target tables [T][n]
     long long zt_off;                      // logits at the targets, [T][n]
-    long long part_off;                    // (max, sum of exp) per token and 128 columns, [columns / 128][T]
-    int stat_cols;                         // columns / 128
+    long long part_off;                    // (max, sum of exp) per token and 128 columns or warp, [stat_cols][T]
+    int stat_cols;                         // pairs per token
     long long g_off[2], ldg;               // dZ of a piece, [parts][T][ldg]; two of them, in turn
     int dh_splits, dh_kb;                  // dH tiles: parts of a piece along the vocabulary, k-blocks each
     long long acc_off, ldacc;              // FP32 sums of dH, [dh_splits][T][ldacc]
@@ -73,6 +74,21 @@ cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const floa
 // dst = sum of `splits` FP32 matrices + beta * dst (splits == 0: dst = beta * dst), rows x cols.
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
                                 float beta, void *dst, long long ldd, int dtype, cudaStream_t stream);
+
+// Losses of a few FP32 tokens without tensor cores (vocab_few.cu): the (max, sum) pair and the targets' logits of
+// every warp's range of the vocabulary.
+struct VocabFewParams {
+    int T, V, D;
+    const float *H, *W;
+    long long ldh, ldw;
+    float scale;
+    VocabTargets t;
+    float2 *part;  // [vocab_few_warps][T]
+    float *zt;
+    int rows;  // of the vocabulary per warp (set by the launch)
+};
+int vocab_few_warps(int T, int num_sms);
+cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, cudaStream_t stream);
 
 // Tile kernel (vocab_kernels.cu): one launch's tiles.
 enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };

@@ -13,6 +13,9 @@ namespace {
 // two pieces' dZ stay a small part of the logits' size while a launch still has many rounds of tiles.
 constexpr long long kPieceBytes = 256LL << 20;
 
+// FP32 losses of up to this many tokens read W as it is.
+constexpr int kFewTokens = 16;
+
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 }  // namespace
@@ -52,8 +55,9 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.workers = w.ctas == 2 ? pairs : q.num_sms;
     const int bm = 128 * w.ctas;
 
-    w.copy_h = f32 || !(q.align_flags & 1);
-    w.copy_w = f32 || !(q.align_flags & 2);
+    w.few = f32 && !grad && T <= kFewTokens;
+    w.copy_h = !w.few && (f32 || !(q.align_flags & 1));
+    w.copy_w = !w.few && (f32 || !(q.align_flags & 2));
     w.ldh = w.ldw = round_up(q.D, 8);
     if (w.copy_h) w.h_off = take(w.parts * T * w.ldh * 2);
     if (w.copy_w) w.w_off = take(w.parts * static_cast<long long>(q.V) * w.ldw * 2);
@@ -64,7 +68,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
     }
     int launches = w.copy_h + w.copy_w + (q.n > 0);
     if (!grad) {
-        w.stat_cols = 2 * ((q.V + kVocabBN - 1) / kVocabBN);
+        w.stat_cols = w.few ? vocab_few_warps(q.T, q.num_sms) : 2 * ((q.V + kVocabBN - 1) / kVocabBN);
         w.zt_off = take(T * std::max(1, q.n) * 4);
         w.part_off = take(T * w.stat_cols * 8);
         w.pub.pieces = 1;
