@@ -34,6 +34,8 @@ struct Call {
     void *dH = nullptr, *dW = nullptr;
     int lddh = 0, lddw = 0;
     cudaStream_t stream;
+    mutable int launched = 0;  // kernels of this call so far: all but the first are dependents of the one before
+    bool dependent() const { return launched++ > 0; }
 };
 
 bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -54,7 +56,7 @@ int check(const Call &c, bool grad)
     if (rc != SGEMM_OK) return rc;
     const unsigned size = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     if (c.ldh < c.D || c.ldw < c.D || (c.n > 0 && c.ldn < c.n)) return SGEMM_ERR_INVALID_VALUE;
-    if (!std::isfinite(c.scale) || !std::isfinite(c.mult) || c.mult == 0.0f || !std::isfinite(c.beta))
+    if (!(c.scale > 0.0f) || !std::isfinite(c.scale) || !std::isfinite(c.mult) || c.mult == 0.0f || !std::isfinite(c.beta))
         return SGEMM_ERR_INVALID_VALUE;  // mult: a temperature whose square leaves FP32's range
     for (const void *p : {c.H, c.W, static_cast<const void *>(c.dH), static_cast<const void *>(c.dW)})
         if (!aligned(p, size)) return SGEMM_ERR_INVALID_VALUE;
@@ -98,7 +100,7 @@ int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src,
         return make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
     void *dst = static_cast<char *>(c.h->workspace) + off;
     const long long part = rows * ldp;
-    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.stream) != cudaSuccess)
+    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.dependent(), c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return make_map(c.h, map, dst, SGEMM_DTYPE_BF16, c.D, rows, ldp, w.parts, part, false);
 }
@@ -119,9 +121,11 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     p->dtype = c.dtype;
     p->parts = w.parts;
     p->products = w.products;
-    // Segments (vocab_kernels.cu): 512 deep for the logits, 256 for FP32 operands, whole for sums rounded to bfloat16.
-    p->seg_z = w.parts == 1 ? 8 : 4;
-    p->seg_g = w.parts == 1 ? 1 << 24 : 4;
+    // Segments (vocab_kernels.cu): 1024 deep for the logits of a loss, 256 for FP32 operands, whole for what is rounded
+    // to bfloat16.
+    const int whole = 1 << 24;
+    p->seg_z = w.parts > 1 ? 4 : c.dH == nullptr && c.dW == nullptr ? 16 : whole;
+    p->seg_g = w.parts > 1 ? 4 : whole;
     p->scale = c.scale;
     p->lse = c.lse;
     p->dloss = c.dloss;
@@ -135,7 +139,8 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
         p->t.id = tid;
         p->t.q = tq;
         p->t.logq = tlogq;
-        if (launch_vocab_targets(c.T, c.V, c.n, c.ids, c.logits, c.ldn, c.scale, tid, tq, tlogq, c.stream) != cudaSuccess)
+        if (launch_vocab_targets(c.T, c.V, c.n, c.ids, c.logits, c.ldn, c.scale, tid, tq, tlogq, c.dependent(),
+                                 c.stream) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
     }
     return SGEMM_OK;
@@ -166,8 +171,8 @@ int run_loss(const Call &c)
         const VocabFewParams f{c.T, c.V, c.D, static_cast<const float *>(c.H), static_cast<const float *>(c.W), c.ldh,
                                c.ldw, c.scale, p.t, p.part, p.zt, 0};
         const bool vec = problem(c).align_flags == 3;
-        if (launch_vocab_few(f, vec, c.h->num_sms, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) {
+        if (launch_vocab_few(f, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
         return SGEMM_ERR_LAUNCH;
     }
     if (launch_vocab_combine(c.T, c.V, p.t, p.part, w.stat_cols, p.zt, c.mult, c.loss, c.lse_out, c.stream) != cudaSuccess)
@@ -184,7 +189,7 @@ int run_grad(const Call &c)
     if (!g.ok) return SGEMM_ERR_CUDA;
     if (c.T == 0) {
         if (c.dW != nullptr && launch_vocab_finish(c.V, c.D, nullptr, 0, 0, 0, c.beta, c.dW, c.lddw, c.dtype,
-                                                   c.stream) != cudaSuccess)
+                                                   c.dependent(), c.stream) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
         return SGEMM_OK;
     }
@@ -244,10 +249,10 @@ int run_grad(const Call &c)
         const int others = p.dw_items + p.z_items, rem = p.dh_items % w.workers;
         const int cost = vocab_cost(c.dW != nullptr ? c.T : c.D);
         p.dh_extra = p.dh_items > 0 && rem > 0 ? std::min((w.dh_kb + cost / 2) / cost, others / (w.workers - rem)) : 0;
-        if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
     if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, acc, w.ldacc, acc_split, w.dh_splits, c.beta, c.dH, c.lddh,
-                                               c.dtype, c.stream) != cudaSuccess)
+                                               c.dtype, c.dependent(), c.stream) != cudaSuccess)
         return SGEMM_ERR_LAUNCH;
     return SGEMM_OK;
 }

@@ -19,6 +19,8 @@
 namespace sgemm_impl {
 namespace {
 
+using namespace sgemm_dev;
+
 constexpr int WARPS = 8;
 constexpr int R = 8;
 constexpr float kInf = __builtin_huge_valf();
@@ -77,6 +79,8 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
     const int va = static_cast<int>(min(static_cast<long long>(gw) * p.rows, static_cast<long long>(p.V)));
     const int vb = static_cast<int>(min(va + static_cast<long long>(p.rows), static_cast<long long>(p.V)));
     const int whole = p.D / 128 * 128;
+    pdl_wait();
+    pdl_trigger();
     for (int t0 = 0; t0 < p.T; t0 += TG) {
         const float *h[TG];
 #pragma unroll
@@ -131,17 +135,19 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             for (int i = 0; i < PER; ++i) sums[warp][lane * N / 32 + i] = acc[i];
             __syncwarp();
             if (!mine) continue;
-            float z[R], top = m;
+            // as powers of two, the rounded maximum M being what is kept: exp(z - m) = 2^(k sum - M)
+            float z[R], best = -kInf;
             const int rows = min(R, vb - v);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                z[r] = r < rows ? p.scale * sums[warp][lane * R + r] : -kInf;
-                top = fmaxf(top, z[r]);
+                z[r] = r < rows ? sums[warp][lane * R + r] : -kInf;
+                best = fmaxf(best, z[r]);
             }
+            const float k = p.scale * 1.4426950408889634f, top = fmaxf(m, k * best);
             const float base = top == -kInf ? 0.0f : top;
-            s *= expf(m - base);
+            s *= exp2f(m - base);
 #pragma unroll
-            for (int r = 0; r < R; ++r) s += expf(z[r] - base);
+            for (int r = 0; r < R; ++r) s += exp2f(fmaf(z[r], k, -base));
             m = top;
             if (p.t.labels != nullptr) {
                 const long long y = p.t.labels[token];
@@ -162,28 +168,25 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
 int warps_per_sm(int T) { return WARPS * (T > 4 ? 1 : 2); }
 
 template <int TG>
-cudaError_t launch(const VocabFewParams &p, bool vec, int blocks, cudaStream_t stream)
+cudaError_t launch(const VocabFewParams &p, bool vec, int blocks, bool dependent, cudaStream_t stream)
 {
-    if (vec)
-        vocab_few_kernel<TG, true><<<blocks, WARPS * 32, 0, stream>>>(p);
-    else
-        vocab_few_kernel<TG, false><<<blocks, WARPS * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(dependent, vec ? vocab_few_kernel<TG, true> : vocab_few_kernel<TG, false>, dim3(blocks),
+                         dim3(WARPS * 32), 0, stream, p);
 }
 
 }  // namespace
 
 int vocab_few_warps(int T, int num_sms) { return warps_per_sm(T) * num_sms; }
 
-cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, cudaStream_t stream)
+cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, bool dependent, cudaStream_t stream)
 {
     const int warps = vocab_few_warps(p.T, num_sms);
     p.rows = (p.V + warps - 1) / warps;
     const int blocks = warps / WARPS;
-    if (p.T > 8) return launch<16>(p, vec, blocks, stream);
-    if (p.T > 4) return launch<8>(p, vec, blocks, stream);
-    if (p.T > 2) return launch<4>(p, vec, blocks, stream);
-    return launch<2>(p, vec, blocks, stream);
+    if (p.T > 8) return launch<16>(p, vec, blocks, dependent, stream);
+    if (p.T > 4) return launch<8>(p, vec, blocks, dependent, stream);
+    if (p.T > 2) return launch<4>(p, vec, blocks, dependent, stream);
+    return launch<2>(p, vec, blocks, dependent, stream);
 }
 
 }  // namespace sgemm_impl

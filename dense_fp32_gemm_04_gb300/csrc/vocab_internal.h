@@ -65,15 +65,18 @@ inline int vocab_cost(int k) { return k > 6 * kVocabBK ? (k + kVocabBK - 1) / kV
 int validate_vocab(const VocabProblem &q);
 VocabLayout vocab_layout(const VocabProblem &q);
 
+// All launches: dependent = launched as a programmatic dependent of the call's previous kernel, whose end it waits
+// for; a call's first kernel is not.
 // Row kernels (vocab_rows.cu).
 cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, const float *logits, long long ldn,
-                                 float scale, int *tid, float *tq, float *tlogq, cudaStream_t stream);
+                                 float scale, int *tid, float *tq, float *tlogq, bool dependent,
+                                 cudaStream_t stream);
 // lse and loss of each token from the columns' (max, sum) pairs and the logits at its targets.
 cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
                                  float mult, float *loss, float *lse, cudaStream_t stream);
 // dst = sum of `splits` FP32 matrices + beta * dst (splits == 0: dst = beta * dst), rows x cols.
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
-                                float beta, void *dst, long long ldd, int dtype, cudaStream_t stream);
+                                float beta, void *dst, long long ldd, int dtype, bool dependent, cudaStream_t stream);
 
 // Losses of a few FP32 tokens without tensor cores (vocab_few.cu): the (max, sum) pair and the targets' logits of
 // every warp's range of the vocabulary.
@@ -88,7 +91,7 @@ struct VocabFewParams {
     int rows;  // of the vocabulary per warp (set by the launch)
 };
 int vocab_few_warps(int T, int num_sms);
-cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, cudaStream_t stream);
+cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, bool dependent, cudaStream_t stream);
 
 // Tile kernel (vocab_kernels.cu): one launch's tiles.
 enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };
@@ -129,9 +132,9 @@ int vocab_max_pairs();
 struct VocabMaps {
     CUtensorMap H, W, G, Gw, acc, dW;
 };
-cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers,
+cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers, bool dependent,
                                cudaStream_t stream);
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
-                               long long ldd, long long part, cudaStream_t stream);
+                               long long ldd, long long part, bool dependent, cudaStream_t stream);
 
 }  // namespace sgemm_impl

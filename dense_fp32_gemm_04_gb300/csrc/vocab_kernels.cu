@@ -59,7 +59,8 @@ static_assert(REGS_ISSUE + 2 * REGS_EPILOGUE <= 3 * REGS_LAUNCH, "an exchange ab
 constexpr int COLS = 128;      // accumulator columns of one epilogue thread
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kWarpStaging = 32 * 128;  // bytes: 32 rows of 128 (64 bfloat16 or 32 floats)
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f;                              // log2(e) in two FP32 parts
+constexpr float kLog2eLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 constexpr float kInf = __builtin_huge_valf();
 
 template <int CTAS>
@@ -306,82 +307,126 @@ __device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg,
     }
 }
 
-// Targets of one row: the entries with ids in [c0, c0 + 128) in turn. f(column - c0, entry, weight).
-template <typename F>
-__device__ __forceinline__ void for_targets(const VocabTileParams &p, long long row, bool live, int c0, F f)
+// What a thread needs to know of its row before the tile is there: fetched while the products run.
+struct Row {
+    int entry, id;   // the first target with an id of at least the tile's first column, and that id
+    float q;
+    float g, lse;    // dZ: the loss' gradient (0 for a masked token), log-sum-exp
+    bool used;
+};
+
+__device__ __forceinline__ void load_target(const VocabTileParams &p, Row &r, long long row)
 {
-    if (p.t.labels != nullptr) {
-        if (!live) return;
-        const long long y = p.t.labels[row];
-        if (y >= c0 && y < c0 + COLS && y < p.V) f(static_cast<int>(y - c0), 0, 1.0f);
-        return;
-    }
-    if (!live) return;
-    const int *id = p.t.id + row * p.t.n;
-    int lo = 0, hi = p.t.n;  // first entry with id >= c0
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (id[mid] < c0)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    for (; lo < p.t.n; ++lo) {
-        const int y = id[lo];
-        if (y >= c0 + COLS || y >= p.V) break;  // kNoTarget ends the list too
-        f(y - c0, lo, p.t.q[row * p.t.n + lo]);
+    r.id = kNoTarget;
+    if (r.entry < p.t.n) {
+        r.id = p.t.id[row * p.t.n + r.entry];
+        r.q = p.t.q[row * p.t.n + r.entry];
     }
 }
 
-// Z tile of a loss call: (max, sum of exp) of the thread's columns, and the logits at its targets.
-__device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
+__device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row, int c0, bool dz)
 {
-    const bool live = row < p.T;
+    Row r{};
+    r.id = kNoTarget;
+    if (row >= p.T) return r;
+    if (p.t.labels != nullptr) {
+        const long long y = p.t.labels[row];
+        r.used = y >= 0 && y < p.V;
+        if (r.used && y >= c0) r.id = static_cast<int>(y);
+        r.q = 1.0f;
+    } else {
+        const int *id = p.t.id + row * p.t.n;
+        if (dz) r.used = id[0] != kNoTarget;
+        int hi = p.t.n;
+        while (r.entry < hi) {
+            const int mid = (r.entry + hi) >> 1;
+            if (id[mid] < c0)
+                r.entry = mid + 1;
+            else
+                hi = mid;
+        }
+        load_target(p, r, row);
+    }
+    if (dz) {
+        if (r.used) r.g = p.dloss[row];
+        r.lse = p.lse[row];
+    }
+    return r;
+}
+
+// f(column - c0) for the row's targets in [c0, c0 + 128) one after the other; r.entry and r.q are the target's.
+template <typename F>
+__device__ __forceinline__ void for_targets(const VocabTileParams &p, Row &r, long long row, int c0, F f)
+{
+    while (r.id < c0 + COLS) {  // (kNoTarget, and V and above, are past every tile)
+        f(r.id - c0);
+        if (p.t.labels != nullptr) return;
+        ++r.entry;
+        load_target(p, r, row);
+    }
+}
+
+// 32 of the thread's columns, as the TMEM loads take them.
+__device__ __forceinline__ float (&columns(float (&acc)[COLS], int cb))[32]
+{
+    return reinterpret_cast<float(&)[32]>(acc[cb * 32]);
+}
+
+// Z tile of a loss call: the softmax statistics of the thread's columns, and the logits at its targets. z = scale * acc;
+// the exponentials are powers of two, exp(z - m) = 2^(k acc - M) with k = scale log2(e) and M = k max(acc) rounded: M is
+// what the pair holds, so its rounding costs nothing.
+__device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
+{
     const int cols = p.V - c0;  // columns of the vocabulary from c0 on
-    float m = -kInf;
+    if (cols < COLS) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-        z[i] = i < cols ? z[i] * p.scale : -kInf;
-        m = fmaxf(m, z[i]);
+        for (int i = 0; i < COLS; ++i) z[i] = i < cols ? z[i] : -kInf;
     }
-    const float base = m == -kInf ? 0.0f : m;
-    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    float m[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-    for (int i = 0; i < COLS; i += 4) {
-        s0 += exp2_approx((z[i] - base) * kLog2e);
-        s1 += exp2_approx((z[i + 1] - base) * kLog2e);
-        s2 += exp2_approx((z[i + 2] - base) * kLog2e);
-        s3 += exp2_approx((z[i + 3] - base) * kLog2e);
+    for (int i = 0; i < COLS; ++i) m[i & 3] = fmaxf(m[i & 3], z[i]);
+    const float k = p.scale * kLog2e, top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    const float base = top == -kInf ? 0.0f : -top;
+    const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(base, base);
+    unsigned long long s2[4] = {};
+#pragma unroll
+    for (int i = 0; i < COLS; i += 2) {
+        float x, y;
+        unpack_f32x2(fma_f32x2(pack_f32x2(z[i], z[i + 1]), k2, b2), x, y);
+        s2[i / 2 & 3] = add_f32x2(s2[i / 2 & 3], pack_f32x2(exp2_approx(x), exp2_approx(y)));
     }
-    if (live) p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(m, (s0 + s1) + (s2 + s3));
-    for_targets(p, row, live, c0, [&](int at, int entry, float) {
+    float x, y;
+    unpack_f32x2(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), x, y);
+    if (row < p.T) p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(top, x + y);
+    for_targets(p, r, row, c0, [&](int at) {
         float x = 0.0f;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
-        p.zt[row * p.t.n + entry] = x;
+        p.zt[row * p.t.n + r.entry] = p.scale * x;
     });
 }
 
 // Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q). Rows past T and columns past
 // the vocabulary hold what no copy of the products reads.
-__device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], long long row, int c0)
+__device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
-    const bool live = row < p.T;
-    bool used = false;
-    float g = 0.0f, l = 0.0f;
-    if (live) {
-        const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
-        used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
-        if (used) g = p.dloss[row];
-        l = p.lse[row];
-    }
+    // exp(z - lse) = 2^(k acc - L) 2^-l with L + l = lse log2(e), L rounded and l its remainder: l goes into the factor.
+    const float k = p.scale * kLog2e, L = r.lse * kLog2e;
+    const float l = fmaf(r.lse, kLog2e, -L) + r.lse * kLog2eLow;
+    const float g = r.g * exp2_approx(-l);
+    const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(-L, -L), g2 = pack_f32x2(g, g);
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-        const float e = g * exp2_approx((z[i] * p.scale - l) * kLog2e);
-        z[i] = used ? e : 0.0f;  // a masked token's dZ is 0 whatever its logits are
+    for (int i = 0; i < COLS; i += 2) {
+        float x, y;
+        unpack_f32x2(fma_f32x2(pack_f32x2(z[i], z[i + 1]), k2, b2), x, y);
+        unpack_f32x2(mul_f32x2(pack_f32x2(exp2_approx(x), exp2_approx(y)), g2), z[i], z[i + 1]);
     }
-    for_targets(p, row, live, c0, [&](int at, int, float q) {
-        const float t = g * q;
+    if (!r.used) {  // a masked token's dZ is 0 whatever its logits are
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) z[i] = 0.0f;
+    }
+    for_targets(p, r, row, c0, [&](int at) {
+        const float t = r.g * r.q;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) z[i] -= i == at ? t : 0.0f;
     });
@@ -449,6 +494,7 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
             }
         }
     }
+    pdl_trigger();  // every copy is issued: the call's next kernel may become resident
     // Drain, as in the TF32 kernel: every issued copy has landed (rank 0's barriers count both
     // CTAs'), and unless aborted the MMAs that read it have committed.
     for (int s = 0; s < STAGES; ++s) {
@@ -560,6 +606,10 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         float acc[COLS];
         const int seg = segment_blocks(p, w.kind);
+        const int r0 = w.m0 + static_cast<int>(rank) * 128 + quarter * 32;  // the warp's first row
+        const int c0 = w.n0 + half * COLS;
+        Row r{};
+        if (w.kind == kVocabLoss || w.kind == kVocabDz) r = load_row(p, r0 + lane, p.z_v0 + c0, w.kind == kVocabDz);
         for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
@@ -572,14 +622,23 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             tc_fence_after_sync();
             const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(buf * BN + half * COLS);
+            if (s0 == w.kb0) {
 #pragma unroll
-            for (int cb = 0; cb < COLS / 32; ++cb) {
-                uint32_t v[32];
-                tmem_ld_32(t + cb * 32, v);
-                tmem_wait_ld_32(v);
+                for (int cb = 0; cb < COLS / 32; ++cb) tmem_ld_32(t + cb * 32, columns(acc, cb));
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    acc[cb * 32 + i] = s0 == w.kb0 ? __uint_as_float(v[i]) : acc[cb * 32 + i] + __uint_as_float(v[i]);
+                for (int cb = 0; cb < COLS / 32; ++cb) tmem_wait_ld_32(columns(acc, cb));
+            } else {
+#pragma unroll
+                for (int cb = 0; cb < COLS / 32; ++cb) {
+                    float v[32];
+                    tmem_ld_32(t + cb * 32, v);
+                    tmem_wait_ld_32(v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float *x = acc + cb * 32 + i;
+                        unpack_f32x2(add_f32x2(pack_f32x2(x[0], x[1]), pack_f32x2(v[i], v[i + 1])), x[0], x[1]);
+                    }
+                }
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -591,10 +650,8 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             }
         }
         if (!ok) break;
-        const int r0 = w.m0 + static_cast<int>(rank) * 128 + quarter * 32;  // the warp's first row
-        const int c0 = w.n0 + half * COLS;
         if (w.kind == kVocabLoss) {
-            leave_loss(p, acc, r0 + lane, p.z_v0 + c0);
+            leave_loss(p, acc, r, r0 + lane, p.z_v0 + c0);
             continue;
         }
         // the rest are rows of a matrix: rows from `row` and columns from c0 of the map, as FP32 or in bfloat16 parts
@@ -603,7 +660,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         int row = r0, cols = p.D, parts = 1;
         bool inside = r0 < p.T;
         if (w.kind == kVocabDz) {
-            make_dz(p, acc, r0 + lane, p.z_v0 + c0);
+            make_dz(p, acc, r, r0 + lane, p.z_v0 + c0);
             map = &maps.Gw;
             cols = static_cast<int>(p.ldg);
             parts = p.parts;
@@ -696,6 +753,7 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
         if (!same_layout && threadIdx.x == 0) raise_abort(bars, p, kLayoutCode | kWherePairLayout);
     }
 
+    pdl_wait();  // the call's previous kernel is complete
     // Where the pair's layouts differ both CTAs see it: no copies, no MMAs.
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
@@ -730,6 +788,8 @@ __global__ void __launch_bounds__(256)
 vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, __nv_bfloat16 *__restrict__ dst,
                    long long ldd, long long part)
 {
+    pdl_wait();
+    pdl_trigger();
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (r >= rows) return;
     const E *s = src + r * ld;
@@ -770,15 +830,15 @@ vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, 
 
 template <typename E, int PARTS>
 cudaError_t launch_parts(const E *src, long long ld, int rows, int cols, __nv_bfloat16 *dst, long long ldd,
-                         long long part, cudaStream_t stream)
+                         long long part, bool dependent, cudaStream_t stream)
 {
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld * sizeof(E) % 16 == 0;
     const dim3 grid((rows + 3) / 4), block(64, 4);
     if (vec)
-        vocab_parts_kernel<E, PARTS, 8><<<grid, block, 0, stream>>>(src, ld, rows, cols, dst, ldd, part);
-    else
-        vocab_parts_kernel<E, PARTS, 2><<<grid, block, 0, stream>>>(src, ld, rows, cols, dst, ldd, part);
-    return cudaGetLastError();
+        return launch_kernel(dependent, vocab_parts_kernel<E, PARTS, 8>, grid, block, 0, stream, src, ld, rows, cols, dst,
+                             ldd, part);
+    return launch_kernel(dependent, vocab_parts_kernel<E, PARTS, 2>, grid, block, 0, stream, src, ld, rows, cols, dst, ldd,
+                         part);
 }
 
 template <int CTAS>
@@ -820,26 +880,26 @@ int vocab_max_pairs()
     return clusters;
 }
 
-cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers,
+cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers, bool dependent,
                                cudaStream_t stream)
 {
     const int n = static_cast<int>(std::min<long long>(static_cast<long long>(p.dh_items) + p.dw_items + p.z_items, workers));
     if (ctas == 2)
-        return launch_kernel_cluster(false, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream,
+        return launch_kernel_cluster(dependent, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream,
                                      maps, p);
-    return launch_kernel(false, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, maps, p);
+    return launch_kernel(dependent, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, maps, p);
 }
 
 cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
-                               long long ldd, long long part, cudaStream_t stream)
+                               long long ldd, long long part, bool dependent, cudaStream_t stream)
 {
     __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst);
     if (dtype == SGEMM_DTYPE_BF16)
         return launch_parts<__nv_bfloat16, 1>(static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, d, ldd, part,
-                                              stream);
+                                              dependent, stream);
     const float *f = static_cast<const float *>(src);
-    return parts == 2 ? launch_parts<float, 2>(f, ld, rows, cols, d, ldd, part, stream)
-                      : launch_parts<float, 3>(f, ld, rows, cols, d, ldd, part, stream);
+    return parts == 2 ? launch_parts<float, 2>(f, ld, rows, cols, d, ldd, part, dependent, stream)
+                      : launch_parts<float, 3>(f, ld, rows, cols, d, ldd, part, dependent, stream);
 }
 
 }  // namespace sgemm_impl

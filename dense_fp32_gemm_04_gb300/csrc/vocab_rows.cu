@@ -7,11 +7,14 @@
 
 #include <algorithm>
 
+#include "device_ptx.cuh"
 #include "sgemm_internal.h"
 #include "vocab_internal.h"
 
 namespace sgemm_impl {
 namespace {
+
+using namespace sgemm_dev;
 
 constexpr float kInf = __builtin_huge_valf();
 
@@ -28,6 +31,8 @@ vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const floa
     __shared__ int s_id[SGEMM_DISTILL_MAX_ENTRIES];
     __shared__ float s_x[SGEMM_DISTILL_MAX_ENTRIES];
     __shared__ float s_red[2][THREADS / 32];
+    pdl_wait();
+    pdl_trigger();
     const long long row = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float best = -kInf;
@@ -80,7 +85,7 @@ __device__ __forceinline__ void fold(float &m, float &s, float m2, float s2)
         s += s2;
         return;
     }
-    s = s * expf(m - top) + s2 * expf(m2 - top);
+    s = s * exp2f(m - top) + s2 * exp2f(m2 - top);
     m = top;
 }
 
@@ -94,6 +99,7 @@ vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ pa
     const int r = threadIdx.x % ROWS, l = threadIdx.x / ROWS;
     const long long first = static_cast<long long>(blockIdx.x) * ROWS;
     float m = -kInf, s = 0.0f;
+    pdl_wait();
     if (first + r < T) {
         const float2 *row = part + first + r;
 #pragma unroll 4
@@ -120,7 +126,7 @@ vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ pa
         m = am;
         s = as;
     }
-    const float total = m + logf(s);
+    const float total = (m + log2f(s)) * 0.6931471805599453f;  // m counts powers of two
     float sum = 0.0f;
     if (t.labels != nullptr) {
         const long long y = t.labels[row];
@@ -149,6 +155,7 @@ vocab_finish_kernel(int cols, const float *__restrict__ acc, long long ldacc, lo
     const long long r = blockIdx.x;
     const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (c >= cols) return;
+    pdl_wait();
     float x[4] = {};
     const float *a = acc + r * ldacc + c;
 #pragma unroll 4
@@ -169,10 +176,11 @@ vocab_finish_kernel(int cols, const float *__restrict__ acc, long long ldacc, lo
 }  // namespace
 
 cudaError_t launch_vocab_targets(int T, int V, int n, const long long *ids, const float *logits, long long ldn,
-                                 float scale, int *tid, float *tq, float *tlogq, cudaStream_t stream)
+                                 float scale, int *tid, float *tq, float *tlogq, bool dependent,
+                                 cudaStream_t stream)
 {
-    vocab_targets_kernel<128><<<T, 128, 0, stream>>>(V, n, ids, logits, ldn, scale, tid, tq, tlogq);
-    return cudaGetLastError();
+    return launch_kernel(dependent, vocab_targets_kernel<128>, dim3(T), dim3(128), 0, stream, V, n, ids, logits, ldn, scale,
+                         tid, tq, tlogq);
 }
 
 cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const float2 *part, int parts, const float *zt,
@@ -180,23 +188,21 @@ cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const floa
 {
     // eight rows per block read whole sectors; below a block of them per SM more lanes per row are worth more
     if (T > 1024)
-        vocab_combine_kernel<8><<<(T + 7) / 8, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
-    else
-        vocab_combine_kernel<2><<<(T + 1) / 2, kCombineThreads, 0, stream>>>(T, V, t, part, parts, zt, mult, loss, lse);
-    return cudaGetLastError();
+        return launch_kernel(true, vocab_combine_kernel<8>, dim3((T + 7) / 8), dim3(kCombineThreads), 0, stream, T, V, t,
+                             part, parts, zt, mult, loss, lse);
+    return launch_kernel(true, vocab_combine_kernel<2>, dim3((T + 1) / 2), dim3(kCombineThreads), 0, stream, T, V, t, part,
+                         parts, zt, mult, loss, lse);
 }
 
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
-                                float beta, void *dst, long long ldd, int dtype, cudaStream_t stream)
+                                float beta, void *dst, long long ldd, int dtype, bool dependent, cudaStream_t stream)
 {
     const dim3 grid(rows, (cols + 1023) / 1024);
     if (dtype == SGEMM_DTYPE_BF16)
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(cols, acc, ldacc, split, splits, beta,
-                                                      static_cast<__nv_bfloat16 *>(dst), ldd);
-    else
-        vocab_finish_kernel<<<grid, 256, 0, stream>>>(cols, acc, ldacc, split, splits, beta, static_cast<float *>(dst),
-                                                      ldd);
-    return cudaGetLastError();
+        return launch_kernel(dependent, vocab_finish_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, cols, acc, ldacc,
+                             split, splits, beta, static_cast<__nv_bfloat16 *>(dst), ldd);
+    return launch_kernel(dependent, vocab_finish_kernel<float>, grid, dim3(256), 0, stream, cols, acc, ldacc, split, splits,
+                         beta, static_cast<float *>(dst), ldd);
 }
 
 }  // namespace sgemm_impl

@@ -78,7 +78,7 @@ typedef enum sgemm_dtype {
 
 /*
  * loss[t] and lse[t] (FP32, T each) of the cross entropy; labels: T 64-bit ids.
- * Requirements: T >= 0; V, D >= 1; ldh, ldw >= D; scale finite; pointers non-NULL
+ * Requirements: T >= 0; V, D >= 1; ldh, ldw >= D; scale > 0 and finite; pointers non-NULL
  * when T > 0 and aligned to their element (8 bytes for labels). Any violation
  * returns SGEMM_ERR_INVALID_VALUE; SGEMM_ERR_ALLOC if the workspace cannot grow.
  */
