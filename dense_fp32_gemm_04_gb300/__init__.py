@@ -115,6 +115,8 @@ STATIC_SCRATCH_BYTES = 32 << 20
 def library():
     """The loaded C library (loads it on first use; raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -260,6 +262,7 @@ class Sgemm:
         if device is None:
             device = torch.cuda.current_device()
         self.device = device
+        self._torch_device = torch.device("cuda", device)
         h = ctypes.c_void_p()
         _check(library().sgemm_create_for_device(device, ctypes.byref(h)), "sgemm_create_for_device")
         self._h = h
@@ -319,29 +322,26 @@ class Sgemm:
         """Checked operands of a vocabulary loss: (T, V, D, dtype), H and W arguments."""
         import torch
 
-        for t, name in ((H, "H"), (W, "W")):
-            if not isinstance(t, torch.Tensor) or t.dim() != 2:
-                raise TypeError(f"{name} must be a 2-D torch tensor")
+        if not isinstance(H, torch.Tensor) or not isinstance(W, torch.Tensor) or H.dim() != 2 or W.dim() != 2:
+            raise TypeError("H and W must be 2-D torch tensors")
         T, D = H.shape
         V = W.shape[0]
         pw, ldw = _rows_arg(W, V, D, "W")
         ph, ldh = _rows_arg(H, T, D, "H", like=W)
-        if W.device.index != self.device:
-            raise ValueError(f"the operands are on {W.device}, the handle on cuda:{self.device}")
-        dtype = DTYPE_BF16 if W.dtype == torch.bfloat16 else DTYPE_F32
-        return (T, V, D, dtype), (ph, ldh, pw, ldw)
+        if W.device != self._torch_device:
+            raise ValueError(f"the operands are on {W.device}, the handle on {self._torch_device}")
+        return (T, V, D, DTYPE_BF16 if W.dtype == torch.bfloat16 else DTYPE_F32), (ph, ldh, pw, ldw)
 
-    def _on(self, stream):
-        """Context in which new tensors belong to the stream that the call runs on."""
-        import contextlib
-
+    def _empty(self, shape, dtype, stream):
+        """A new tensor that belongs to the stream the call runs on."""
         import torch
 
         if stream is None:
-            return contextlib.nullcontext()
+            return torch.empty(shape, dtype=dtype, device=self._torch_device)
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        return torch.cuda.stream(stream)
+            stream = torch.cuda.ExternalStream(int(stream), device=self._torch_device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self._torch_device)
 
     def _entries(self, ids, logits, T, like):
         """Checked teacher entries: (n, ids, logits, row stride)."""
@@ -356,22 +356,12 @@ class Sgemm:
             raise ValueError(f"ids and logits have different row strides ({ldi} and {ldl})")
         return n, pi, pl, ldi
 
-    def _loss_outputs(self, T, like, stream):
-        import torch
-
-        with self._on(stream):
-            return (torch.empty(T, dtype=torch.float32, device=like.device),
-                    torch.empty(T, dtype=torch.float32, device=like.device))
-
     def _grad_outputs(self, H, W, dH, dW, beta, need_dH, need_dW, stream):
         """(dH, dW, arguments): outputs are made where they are asked for and not given."""
-        import torch
-
         if beta != 0.0 and ((need_dH and dH is None) or (need_dW and dW is None)):
             raise ValueError("beta != 0 adds to given gradients: pass dH and dW")
-        with self._on(stream):
-            dH = (torch.empty(H.shape, dtype=H.dtype, device=H.device) if dH is None else dH) if need_dH else None
-            dW = (torch.empty(W.shape, dtype=W.dtype, device=W.device) if dW is None else dW) if need_dW else None
+        dH = (self._empty(H.shape, H.dtype, stream) if dH is None else dH) if need_dH else None
+        dW = (self._empty(W.shape, W.dtype, stream) if dW is None else dW) if need_dW else None
         args = ()
         for t, like, name in ((dH, H, "dH"), (dW, W, "dW")):
             args += (None, 0) if t is None else _rows_arg(t, like.shape[0], like.shape[1], name, like=W)
@@ -387,7 +377,7 @@ class Sgemm:
 
         (T, V, D, dtype), operands = self._projection(H, W)
         py = _list_arg(labels, (T,), torch.int64, "labels", W)
-        loss, lse = self._loss_outputs(T, W, stream)
+        loss, lse = self._empty(T, torch.float32, stream), self._empty(T, torch.float32, stream)
         _check(library().sgemm_xent(self._h, T, V, D, dtype, *operands, py, scale, loss.data_ptr(), lse.data_ptr(),
                                     self._stream(stream)), "sgemm_xent")
         return loss, lse
@@ -417,9 +407,11 @@ class Sgemm:
         (-1, say) leaves its entry out, a token without entries is masked. The loss carries the factor
         temperature**2, lse is that of the logits divided by the temperature.
         """
+        import torch
+
         (T, V, D, dtype), operands = self._projection(H, W)
         n, pi, pl, ldn = self._entries(ids, logits, T, W)
-        loss, lse = self._loss_outputs(T, W, stream)
+        loss, lse = self._empty(T, torch.float32, stream), self._empty(T, torch.float32, stream)
         _check(library().sgemm_distill(self._h, T, V, D, dtype, *operands, n, pi, pl, ldn, temperature,
                                        loss.data_ptr(), lse.data_ptr(), self._stream(stream)), "sgemm_distill")
         return loss, lse

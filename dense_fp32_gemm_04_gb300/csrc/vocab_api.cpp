@@ -168,10 +168,9 @@ int run_loss(const Call &c)
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
     if (w.few) {
-        const VocabFewParams f{c.T, c.V, c.D, static_cast<const float *>(c.H), static_cast<const float *>(c.W), c.ldh,
-                               c.ldw, c.scale, p.t, p.part, p.zt, 0};
+        const VocabFewParams f{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0};
         const bool vec = problem(c).align_flags == 3;
-        if (launch_vocab_few(f, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        if (launch_vocab_few(f, c.dtype, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
         return SGEMM_ERR_LAUNCH;
     }

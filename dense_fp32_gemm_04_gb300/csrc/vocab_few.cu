@@ -1,6 +1,8 @@
-// Losses of a few FP32 tokens (scoring calls). The head's bytes are the cost: the
-// tensor-core path would first write W as bfloat16 parts and read those, 4 times
-// its size in all, so here every row of W is read once and multiplied as it is.
+// Losses of a few tokens (scoring calls). The head's bytes are the cost. For FP32
+// the tensor-core path would first write W as bfloat16 parts and read those, 4
+// times its size in all; for bfloat16 its tiles of 128 tokens x 256 entries leave
+// SMs idle or uneven in a single wave. Here every row of W is read once, as it
+// is, by warps with equal shares of the vocabulary.
 //
 // A warp takes a contiguous range of the vocabulary, R rows at a time, its lanes
 // side by side along D, and up to TG tokens at once: R * TG FP32 sums per lane from
@@ -8,6 +10,7 @@
 // reduce-scatter over shuffles, and lane t carries token t's running maximum and
 // sum of exponentials through the range. More than TG tokens are done in groups,
 // each reading the range again (from the L2).
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,25 +28,36 @@ constexpr int WARPS = 8;
 constexpr int R = 8;
 constexpr float kInf = __builtin_huge_valf();
 
-__device__ __forceinline__ float4 load_once(const float *p)
-{
-    float4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "l"(p));
-    return v;
-}
+// Elements of a row per lane and step: 16 bytes where rows are 16-byte aligned, else 4, one of every 32 elements.
+template <typename E, bool VEC>
+constexpr int kPerLane = VEC ? 16 / static_cast<int>(sizeof(E)) : 4;
 
-// Four elements of a row for this lane: 16 bytes of 512 where rows are 16-byte aligned, else one of each 128 bytes.
-template <bool VEC, bool ONCE>
-__device__ __forceinline__ float4 load_four(const float *row, int d, int lane)
+template <typename E, bool VEC, bool ONCE>
+__device__ __forceinline__ void load_part(const E *row, int d, int lane, float (&x)[kPerLane<E, VEC>])
 {
     if constexpr (VEC) {
-        if constexpr (ONCE) return load_once(row + d + 4 * lane);
-        return __ldg(reinterpret_cast<const float4 *>(row + d + 4 * lane));
+        uint4 v;
+        const E *at = row + d + lane * kPerLane<E, VEC>;
+        if constexpr (ONCE)
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "l"(at));
+        else
+            v = __ldg(reinterpret_cast<const uint4 *>(at));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 4) {
+                x[i] = __uint_as_float(u[i]);
+            } else {  // a bfloat16 is the upper half of its FP32
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(row[d + lane + 32 * i]);
     }
-    const float *p = row + d + lane;
-    return make_float4(__ldg(p), __ldg(p + 32), __ldg(p + 64), __ldg(p + 96));
 }
 
 // v[0..N) summed over the warp: afterwards v[0..max(1, N / 32)) of a lane are the sums from
@@ -69,22 +83,24 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[N], int lane)
     }
 }
 
-template <int TG, bool VEC>
+template <typename E, int TG, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(const VocabFewParams p)
 {
+    constexpr int PART = kPerLane<E, VEC>, STEP = 32 * PART;
+    const E *H = static_cast<const E *>(p.H), *W = static_cast<const E *>(p.W);
     constexpr int N = R * TG, PER = N >= 32 ? N / 32 : 1;
     __shared__ float sums[WARPS][N];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gw = blockIdx.x * WARPS + warp;
     const int va = static_cast<int>(min(static_cast<long long>(gw) * p.rows, static_cast<long long>(p.V)));
     const int vb = static_cast<int>(min(va + static_cast<long long>(p.rows), static_cast<long long>(p.V)));
-    const int whole = p.D / 128 * 128;
+    const int whole = p.D / STEP * STEP;
     pdl_wait();
     pdl_trigger();
     for (int t0 = 0; t0 < p.T; t0 += TG) {
-        const float *h[TG];
+        const E *h[TG];
 #pragma unroll
-        for (int t = 0; t < TG; ++t) h[t] = p.H + min(t0 + t, p.T - 1) * p.ldh;  // past the end: computed, not kept
+        for (int t = 0; t < TG; ++t) h[t] = H + min(t0 + t, p.T - 1) * p.ldh;  // past the end: computed, not kept
         const int token = t0 + lane;
         const bool mine = lane < TG && token < p.T;
         float m = -kInf, s = 0.0f;
@@ -100,34 +116,32 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             }
         }
         for (int v = va; v < vb; v += R) {
-            const float *w[R];
+            const int rows = min(R, vb - v);
+            const E *w[R];  // past the end the last row again: computed, not kept
 #pragma unroll
-            for (int r = 0; r < R; ++r) w[r] = p.W + min(v + r, vb - 1) * p.ldw;
+            for (int r = 0; r < R; ++r) w[r] = W + min(v + r, vb - 1) * p.ldw;
             float acc[N] = {};
 #pragma unroll 2
-            for (int d = 0; d < whole; d += 128) {
-                float4 a[R];
+            for (int d = 0; d < whole; d += STEP) {
+                float a[R][PART];
 #pragma unroll
-                for (int r = 0; r < R; ++r) a[r] = load_four<VEC, true>(w[r], d, lane);
+                for (int r = 0; r < R; ++r) load_part<E, VEC, true>(w[r], d, lane, a[r]);
 #pragma unroll
                 for (int t = 0; t < TG; ++t) {
-                    const float4 b = load_four<VEC, false>(h[t], d, lane);
+                    float b[PART];
+                    load_part<E, VEC, false>(h[t], d, lane, b);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        float &x = acc[t * R + r];
-                        x = fmaf(a[r].x, b.x, x);
-                        x = fmaf(a[r].y, b.y, x);
-                        x = fmaf(a[r].z, b.z, x);
-                        x = fmaf(a[r].w, b.w, x);
-                    }
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int i = 0; i < PART; ++i) acc[t * R + r] = fmaf(a[r][i], b[i], acc[t * R + r]);
                 }
             }
             for (int d = whole + lane; d < p.D; d += 32)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float a = __ldg(w[r] + d);
+                    const float a = static_cast<float>(w[r][d]);
 #pragma unroll
-                    for (int t = 0; t < TG; ++t) acc[t * R + r] = fmaf(a, __ldg(h[t] + d), acc[t * R + r]);
+                    for (int t = 0; t < TG; ++t) acc[t * R + r] = fmaf(a, static_cast<float>(h[t][d]), acc[t * R + r]);
                 }
             reduce_scatter<N>(acc, lane);
             __syncwarp();
@@ -137,7 +151,6 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             if (!mine) continue;
             // as powers of two, the rounded maximum M being what is kept: exp(z - m) = 2^(k sum - M)
             float z[R], best = -kInf;
-            const int rows = min(R, vb - v);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 z[r] = r < rows ? sums[warp][lane * R + r] : -kInf;
@@ -167,26 +180,33 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
 
 int warps_per_sm(int T) { return WARPS * (T > 4 ? 1 : 2); }
 
-template <int TG>
+template <typename E, int TG>
 cudaError_t launch(const VocabFewParams &p, bool vec, int blocks, bool dependent, cudaStream_t stream)
 {
-    return launch_kernel(dependent, vec ? vocab_few_kernel<TG, true> : vocab_few_kernel<TG, false>, dim3(blocks),
+    return launch_kernel(dependent, vec ? vocab_few_kernel<E, TG, true> : vocab_few_kernel<E, TG, false>, dim3(blocks),
                          dim3(WARPS * 32), 0, stream, p);
+}
+
+template <typename E>
+cudaError_t launch_type(const VocabFewParams &p, bool vec, int blocks, bool dependent, cudaStream_t stream)
+{
+    if (p.T > 4) return launch<E, 8>(p, vec, blocks, dependent, stream);
+    if (p.T > 2) return launch<E, 4>(p, vec, blocks, dependent, stream);
+    if (p.T > 1) return launch<E, 2>(p, vec, blocks, dependent, stream);
+    return launch<E, 1>(p, vec, blocks, dependent, stream);
 }
 
 }  // namespace
 
 int vocab_few_warps(int T, int num_sms) { return warps_per_sm(T) * num_sms; }
 
-cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, bool dependent, cudaStream_t stream)
+cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms, bool dependent, cudaStream_t stream)
 {
     const int warps = vocab_few_warps(p.T, num_sms);
     p.rows = (p.V + warps - 1) / warps;
     const int blocks = warps / WARPS;
-    if (p.T > 8) return launch<16>(p, vec, blocks, dependent, stream);
-    if (p.T > 4) return launch<8>(p, vec, blocks, dependent, stream);
-    if (p.T > 2) return launch<4>(p, vec, blocks, dependent, stream);
-    return launch<2>(p, vec, blocks, dependent, stream);
+    return dtype == SGEMM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, vec, blocks, dependent, stream)
+                                     : launch_type<float>(p, vec, blocks, dependent, stream);
 }
 
 }  // namespace sgemm_impl

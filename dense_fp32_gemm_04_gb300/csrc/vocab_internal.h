@@ -44,7 +44,7 @@ struct VocabProblem {
 // What a call does, and the byte offsets of the parts of its workspace (those a call does not use are empty).
 struct VocabLayout {
     sgemm_vocab_plan_t pub;
-    bool few;      // a few FP32 tokens: vocab_few.cu, no parts
+    bool few;      // a few tokens: vocab_few.cu, no parts
     int ctas;      // CTAs per worker: 2 = pairs computing 256 x 256 tiles, 1 = 128 x 256
     int workers;
     int parts, products;  // bfloat16 parts of an operand, products of parts
@@ -78,11 +78,11 @@ cudaError_t launch_vocab_combine(int T, int V, const VocabTargets &t, const floa
 cudaError_t launch_vocab_finish(int rows, int cols, const float *acc, long long ldacc, long long split, int splits,
                                 float beta, void *dst, long long ldd, int dtype, bool dependent, cudaStream_t stream);
 
-// Losses of a few FP32 tokens without tensor cores (vocab_few.cu): the (max, sum) pair and the targets' logits of
+// Losses of a few tokens without tensor cores (vocab_few.cu): the (max, sum) pair and the targets' logits of
 // every warp's range of the vocabulary.
 struct VocabFewParams {
     int T, V, D;
-    const float *H, *W;
+    const void *H, *W;
     long long ldh, ldw;
     float scale;
     VocabTargets t;
@@ -91,7 +91,7 @@ struct VocabFewParams {
     int rows;  // of the vocabulary per warp (set by the launch)
 };
 int vocab_few_warps(int T, int num_sms);
-cudaError_t launch_vocab_few(VocabFewParams p, bool vec, int num_sms, bool dependent, cudaStream_t stream);
+cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms, bool dependent, cudaStream_t stream);
 
 // Tile kernel (vocab_kernels.cu): one launch's tiles.
 enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };

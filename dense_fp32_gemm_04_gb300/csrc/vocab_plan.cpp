@@ -13,8 +13,11 @@ namespace {
 // two pieces' dZ stay a small part of the logits' size while a launch still has many rounds of tiles.
 constexpr long long kPieceBytes = 256LL << 20;
 
-// FP32 losses of up to this many tokens read W as it is.
-constexpr int kFewTokens = 16;
+// Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
+// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 69 / 345, 24
+// tokens 263 / 345, 32 tokens 350 / 345; bfloat16 131072 x 4096, 2 tokens 158 / 178, 3 tokens 233 / 177; rows at an odd
+// stride, 50021 x 1531, 8 tokens 86 / 92.
+constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
@@ -55,7 +58,8 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.workers = w.ctas == 2 ? pairs : q.num_sms;
     const int bm = 128 * w.ctas;
 
-    w.few = f32 && !grad && T <= kFewTokens;
+    const int few = f32 ? kFewTokensF32 : q.align_flags == 3 ? kFewTokensBf16 : kFewTokensCopied;
+    w.few = !grad && T <= few;
     w.copy_h = !w.few && (f32 || !(q.align_flags & 1));
     w.copy_w = !w.few && (f32 || !(q.align_flags & 2));
     w.ldh = w.ldw = round_up(q.D, 8);

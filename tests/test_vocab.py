@@ -80,7 +80,7 @@ def test_null_handle_is_refused(lib):
 def test_binding_refuses_what_is_not_a_device_matrix():
     """Type, device and shape errors are raised before the library is called (no GPU needed to see them)."""
     h = sg.Sgemm.__new__(sg.Sgemm)
-    h.device, h._h = 0, None
+    h.device, h._h, h._torch_device = 0, None, torch.device("cuda", 0)
     H, W = torch.zeros(3, 8), torch.zeros(5, 8)
     y = torch.zeros(3, dtype=torch.int64)
     with pytest.raises(TypeError):
