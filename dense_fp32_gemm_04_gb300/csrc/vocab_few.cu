@@ -56,7 +56,7 @@ __device__ __forceinline__ void load_part(const E *row, int d, int lane, float (
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(row[d + lane + 32 * i]);
+        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(__ldg(row + d + lane + 32 * i));
     }
 }
 
@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             for (int d = whole + lane; d < p.D; d += 32)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float a = static_cast<float>(w[r][d]);
+                    const float a = static_cast<float>(__ldg(w[r] + d));
 #pragma unroll
-                    for (int t = 0; t < TG; ++t) acc[t * R + r] = fmaf(a, static_cast<float>(h[t][d]), acc[t * R + r]);
+                    for (int t = 0; t < TG; ++t) acc[t * R + r] = fmaf(a, static_cast<float>(__ldg(h[t] + d)), acc[t * R + r]);
                 }
             reduce_scatter<N>(acc, lane);
             __syncwarp();
