@@ -202,8 +202,12 @@ int run_grad(const Call &c)
     const int elem = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     p.z_kind = kVocabDz;
     p.z_tm = tm;
-    p.ldg = w.ldg;
-    const long long g_part = c.T * w.ldg, acc_split = c.T * w.ldacc;
+    p.g_blocks = w.g_blocks;
+    const long long acc_split = c.T * w.ldacc;
+    // dZ in blocks of 64 entries, T x 64 each: every copy of it is one contiguous piece of memory
+    auto dz_map = [&](CUtensorMap *map, long long off, bool result) {
+        return make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, 64, c.T, 64, w.parts * w.g_blocks, 64LL * c.T, result);
+    };
     float *acc = reinterpret_cast<float *>(ws + w.acc_off);
     p.dW = c.dW;
     p.lddw = c.lddw;
@@ -232,18 +236,13 @@ int run_grad(const Call &c)
             if (c.dH != nullptr) p.dh_items = tm * tn * splits;
             if (c.dW != nullptr) p.dw_items = ceil_div(p.g_vn, bm) * tn;
             p.acc_add = i > 1;
-            // only the piece's own columns: the product's K range ends with them
-            if ((rc = make_map(c.h, &m.G, ws + w.g_off[(i - 1) & 1], SGEMM_DTYPE_BF16, p.g_vn, c.T, w.ldg, w.parts, g_part,
-                               false)) != SGEMM_OK)
-                return rc;
+            if ((rc = dz_map(&m.G, w.g_off[(i - 1) & 1], false)) != SGEMM_OK) return rc;
         }
         if (i < w.pub.pieces) {
             p.z_v0 = i * w.pub.piece;
             p.z_tn = ceil_div(c.V - p.z_v0 < w.pub.piece ? c.V - p.z_v0 : w.pub.piece, kVocabBN);
             p.z_items = tm * p.z_tn;
-            if ((rc = make_map(c.h, &m.Gw, ws + w.g_off[i & 1], SGEMM_DTYPE_BF16, static_cast<int>(w.ldg), c.T, w.ldg,
-                               w.parts, g_part, true)) != SGEMM_OK)
-                return rc;
+            if ((rc = dz_map(&m.Gw, w.g_off[i & 1], true)) != SGEMM_OK) return rc;
         }
         const int others = p.dw_items + p.z_items, rem = p.dh_items % w.workers;
         const int cost = vocab_cost(c.dW != nullptr ? c.T : c.D);

@@ -54,7 +54,8 @@ struct VocabLayout {
     long long zt_off;                      // logits at the targets, [T][n]
     long long part_off;                    // (max, sum of exp) per token and 128 columns or warp, [stat_cols][T]
     int stat_cols;                         // pairs per token
-    long long g_off[2], ldg;               // dZ of a piece, [parts][T][ldg]; two of them, in turn
+    long long g_off[2];                    // dZ of a piece, [parts][g_blocks][T][64]; two of them, in turn
+    int g_blocks;                          // blocks of 64 entries of a piece, in whole tiles
     int dh_splits, dh_kb;                  // dH tiles: parts of a piece along the vocabulary, k-blocks each
     long long acc_off, ldacc;              // FP32 sums of dH, [dh_splits][T][ldacc]
 };
@@ -109,7 +110,7 @@ struct VocabTileParams {
     float2 *part;
     float *zt;
     const float *lse, *dloss;
-    long long ldg;       // columns of dZ's buffer
+    int g_blocks;        // dZ's buffer: blocks of 64 entries per part, [parts][g_blocks][T][64]
     // dH and dW tiles of the piece [g_v0, g_v0 + g_vn), whose dZ an earlier launch left
     int g_v0, g_vn;
     int dw_tn;

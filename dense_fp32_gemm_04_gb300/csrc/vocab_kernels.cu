@@ -221,9 +221,10 @@ __device__ __forceinline__ void send_f32(const CUtensorMap *map, const float (&a
     }
 }
 
-// alpha * columns as bfloat16, 64 per block, in parts: each but the last leaves its remainder (exact in FP32) to the next.
+// alpha * columns as bfloat16, 64 per block, in parts: each but the last leaves its remainder (exact in FP32) to the
+// next. blocks > 0: to a matrix in blocks of 64 columns, `blocks` of them per part.
 __device__ __forceinline__ void send_bf16(const CUtensorMap *map, float (&acc)[COLS], uint32_t stg, int lane, int x,
-                                          int y, int cols, int parts, float alpha)
+                                          int y, int cols, int parts, int blocks, float alpha)
 {
 #pragma unroll
     for (int cb = 0; cb < COLS / 64; ++cb) {
@@ -241,7 +242,10 @@ __device__ __forceinline__ void send_bf16(const CUtensorMap *map, float (&acc)[C
                 }
                 sts128(stg + lane * 128 + ((j ^ (lane & 7)) << 4), v);
             }
-            stage_send(map, stg, lane, x + cb * 64, y, part, false);
+            if (blocks > 0)
+                stage_send(map, stg, lane, 0, y, part * blocks + x / 64 + cb, false);
+            else
+                stage_send(map, stg, lane, x + cb * 64, y, 0, false);
             if (++part == parts) break;
 #pragma unroll
             for (int i = 0; i < 64; ++i) {  // (more than one part: dZ, whose alpha is 1)
@@ -406,8 +410,7 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     });
 }
 
-// Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q). Rows past T and columns past
-// the vocabulary hold what no copy of the products reads.
+// Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q).
 __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
     // exp(z - lse) = 2^(k acc - L) 2^-l with L + l = lse log2(e), L rounded and l its remainder: l goes into the factor.
@@ -421,9 +424,11 @@ __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COL
         unpack_f32x2(fma_f32x2(pack_f32x2(z[i], z[i + 1]), k2, b2), x, y);
         unpack_f32x2(mul_f32x2(pack_f32x2(exp2_approx(x), exp2_approx(y)), g2), z[i], z[i + 1]);
     }
-    if (!r.used) {  // a masked token's dZ is 0 whatever its logits are
+    // a masked token's dZ is 0 whatever its logits are; so is dZ past the vocabulary, which the products do read
+    const int cols = r.used ? p.V - c0 : 0;
+    if (cols < COLS) {
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) z[i] = 0.0f;
+        for (int i = 0; i < COLS; ++i) z[i] = i < cols ? z[i] : 0.0f;
     }
     for_targets(p, r, row, c0, [&](int at) {
         const float t = r.g * r.q;
@@ -471,11 +476,14 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
                     if constexpr (PAIR) full = mapa_shared(full, 0);  // rank 0's barrier
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int x = a_k ? kb * BK : a_r + 64 * j, y = a_k ? a_r + 64 * j : kb * BK;
+                        // H: (k, token, part); dZ, in blocks of 64 entries: (entry, token, block of the part)
+                        const int x = z ? kb * BK : 0;
+                        const int y = a_k ? a_r + 64 * j : kb * BK;
+                        const int b = z ? pa : pa * p.g_blocks + (a_k ? kb : a_r / 64 + j);
                         if constexpr (PAIR)
-                            tma_load_3d_pair(a_dst + j * BOX_BYTES, ta, full, x, y, pa);
+                            tma_load_3d_pair(a_dst + j * BOX_BYTES, ta, full, x, y, b);
                         else
-                            tma_load_3d(a_dst + j * BOX_BYTES, ta, full, x, y, pa);
+                            tma_load_3d(a_dst + j * BOX_BYTES, ta, full, x, y, b);
                     }
 #pragma unroll
                     for (int j = 0; j < S::CTA_N / 64; ++j) {
@@ -657,14 +665,15 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         // the rest are rows of a matrix: rows from `row` and columns from c0 of the map, as FP32 or in bfloat16 parts
         const CUtensorMap *map = &maps.dW;
         const bool wide = w.kind == kVocabDh || (w.kind == kVocabDw && p.dtype == SGEMM_DTYPE_F32);
-        int row = r0, cols = p.D, parts = 1;
+        int row = r0, cols = p.D, parts = 1, blocks = 0;
         bool inside = r0 < p.T;
         if (w.kind == kVocabDz) {
             make_dz(p, acc, r, r0 + lane, p.z_v0 + c0);
             map = &maps.Gw;
-            cols = static_cast<int>(p.ldg);
+            cols = p.g_blocks * 64;
             parts = p.parts;
-            inside = inside && index_ok(c0 + COLS <= p.ldg, p.status, kWhereIdxVocabDz);
+            blocks = p.g_blocks;
+            inside = inside && index_ok(c0 + COLS <= cols, p.status, kWhereIdxVocabDz);
         } else if (w.kind == kVocabDh) {
             map = &maps.acc;
         } else {
@@ -683,7 +692,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         } else if (wide) {
             send_f32(map, acc, stg, lane, c0, row, w.split, cols, w.kind == kVocabDh && p.acc_add, p.alpha);
         } else {
-            send_bf16(map, acc, stg, lane, c0, row, cols, parts, w.kind == kVocabDz ? 1.0f : p.alpha);
+            send_bf16(map, acc, stg, lane, c0, row, cols, parts, blocks, w.kind == kVocabDz ? 1.0f : p.alpha);
         }
     }
     if (lane == 0) bulk_wait();  // the staging area is read and everything is written before the CTA ends

@@ -83,9 +83,9 @@ VocabLayout vocab_layout(const VocabProblem &q)
         const long long piece = std::min<long long>(fit / kVocabBN * kVocabBN, round_up(q.V, kVocabBN));
         w.pub.piece = static_cast<int>(std::min<long long>(piece, q.V));
         w.pub.pieces = static_cast<int>((q.V + piece - 1) / piece);
-        w.ldg = piece;
-        w.g_off[0] = take(w.parts * T * w.ldg * 2);
-        w.g_off[1] = w.pub.pieces > 1 ? take(w.parts * T * w.ldg * 2) : w.g_off[0];
+        w.g_blocks = static_cast<int>(piece / 64);
+        w.g_off[0] = take(w.parts * T * piece * 2);
+        w.g_off[1] = w.pub.pieces > 1 ? take(w.parts * T * piece * 2) : w.g_off[0];
         if (q.dh) {
             // A dH tile's K range is a piece of the vocabulary, the other tiles' are T and D. It is split so far
             // that no part of it takes a worker more than half its share of a launch (the other tiles fill what
