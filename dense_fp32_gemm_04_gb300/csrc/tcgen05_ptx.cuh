@@ -51,8 +51,8 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
-// As mma_tf32, with bfloat16 inputs (K = 16 per instruction).
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// As mma_tf32, with 16-bit inputs of one type, float16 or bfloat16 (K = 16 per instruction).
+__device__ __forceinline__ void mma_16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate)
 {
     asm volatile(
@@ -170,12 +170,12 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_byte_addr, 
     return d;
 }
 
-// Instruction descriptor of tcgen05.mma .kind::f16 with bfloat16 inputs (A and B
-// format 1) and FP32 accumulation; the other fields as in idesc_tf32, A MN-major
-// where a_mn (bit 15).
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+// Instruction descriptor of tcgen05.mma .kind::f16 with FP32 accumulation and A and
+// B both bfloat16 (format 1) or both float16 (format 0, f16); the other fields as
+// in idesc_tf32, A MN-major where a_mn (bit 15).
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool a_mn, bool b_mn, bool f16)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -288,8 +288,8 @@ __device__ __forceinline__ void mma_tf32_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
-// As mma_tf32_pair, with bfloat16 inputs.
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// As mma_tf32_pair, with 16-bit inputs.
+__device__ __forceinline__ void mma_16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate)
 {
     asm volatile(

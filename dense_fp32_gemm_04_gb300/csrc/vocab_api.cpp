@@ -92,17 +92,33 @@ int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int dtype, in
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-// The map of H or W: the caller's matrix, or its parts, which are made first.
+// The maps of H or W, as Z reads it and as the other products do: the caller's matrix, or what is first made of it in
+// the workspace.
 int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src, int rows, int ld, long long off,
-                long long ldp, CUtensorMap *map)
+                long long z_off, float *unscale, CUtensorMap *z_map, CUtensorMap *map)
 {
-    if (!copy)
-        return make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
-    void *dst = static_cast<char *>(c.h->workspace) + off;
-    const long long part = rows * ldp;
-    if (launch_vocab_parts(src, c.dtype, ld, rows, c.D, w.parts, dst, ldp, part, c.dependent(), c.stream) != cudaSuccess)
-        return SGEMM_ERR_LAUNCH;
-    return make_map(c.h, map, dst, SGEMM_DTYPE_BF16, c.D, rows, ldp, w.parts, part, false);
+    char *ws = static_cast<char *>(c.h->workspace);
+    const long long part = rows * w.ldp;
+    int rc = SGEMM_OK;
+    if (w.split) {
+        if (launch_vocab_split(src, ld, rows, c.D, ws + z_off, unscale, copy ? ws + off : nullptr, w.parts, w.ldp,
+                               c.dependent(), c.stream) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+        rc = make_map(c.h, z_map, ws + z_off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, 2, part, false);
+        *map = *z_map;
+        if (rc == SGEMM_OK && copy)
+            rc = make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, w.parts, part, false);
+        return rc;
+    }
+    if (copy) {
+        if (launch_vocab_copy(src, ld, rows, c.D, ws + off, w.ldp, c.dependent(), c.stream) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+        rc = make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, 1, part, false);
+    } else {
+        rc = make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
+    }
+    *z_map = *map;
+    return rc;
 }
 
 // Operands, targets (the distillation's tables are made first) and what every launch of the call shares.
@@ -110,10 +126,16 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
 {
     char *ws = static_cast<char *>(c.h->workspace);
     if (!w.few) {
+        float *hs = reinterpret_cast<float *>(ws + w.hs_off), *vs = reinterpret_cast<float *>(ws + w.ws_off);
         int rc;
-        if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.ldh, &m->H)) != SGEMM_OK) return rc;
-        if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.ldw, &m->W)) != SGEMM_OK) return rc;
+        if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.hz_off, hs, &m->Hz, &m->H)) != SGEMM_OK)
+            return rc;
+        if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.wz_off, vs, &m->Wz, &m->W)) != SGEMM_OK)
+            return rc;
         m->G = m->Gw = m->acc = m->dW = m->W;  // where a call has no such matrix, a valid map that no tile uses
+        p->z_f16 = w.split;
+        p->h_unscale = hs;
+        p->w_unscale = vs;
     }
     p->T = c.T;
     p->V = c.V;
@@ -121,6 +143,7 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     p->dtype = c.dtype;
     p->parts = w.parts;
     p->products = w.products;
+    p->z_products = w.split ? 3 : 1;
     // Segments (vocab_kernels.cu): 1024 deep for the logits of a loss, 256 for FP32 operands, whole for what is rounded
     // to bfloat16.
     const int whole = 1 << 24;

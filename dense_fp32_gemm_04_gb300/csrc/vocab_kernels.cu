@@ -1,5 +1,5 @@
 // Tile kernel of the vocabulary losses on the 5th-generation tensor cores. One
-// persistent kernel computes all three products of bfloat16 operands with FP32
+// persistent kernel computes all three products of 16-bit operands with FP32
 // accumulation, 128 x 256 tiles per CTA or 256 x 256 tiles per CTA pair:
 //   Z   = scale * H W^T   A = H (T x D, K-major), B = W (V x D, K-major); leaves
 //                         the tile as softmax statistics (loss), or as dZ in
@@ -11,17 +11,24 @@
 // vocabulary and the dZ tiles of the next, so the partial last round of one
 // product is filled by another's tiles.
 //
-// FP32 operands are sums of bfloat16 parts (vocab_parts_kernel); a product of
-// three parts each is the six bfloat16 products down to 2^-16 of the leading
-// one, small ones first: the same loop over more slabs.
+// FP32 operands (vocab_split_kernel) are sums of 16-bit parts, a product of them
+// the products of parts down to about 2^-22 of the leading one, small ones first:
+// the same loop over more slabs. For Z, whose operands are rows with one scale
+// each, two float16 parts (22 bits) of the rows scaled by powers of two, 3
+// products; an element far below its row's largest has fewer bits, but in the sum
+// it stands next to the largest. For dH and dW, where dZ spans many orders of
+// magnitude and each row of dW may be made of small ones alone, three bfloat16
+// parts (24 bits at any magnitude), 6 products.
 //
 // Accumulation: the tensor core truncates its FP32 accumulator at every K = 16
 // step (measured: rel. error 4.4e-6 at K = 4096, all of it toward zero), which a
 // logit of 12 would show in its loss. So a tile's K range is cut into segments
-// (512 deep for Z, 256 deep in every product of FP32 operands); the epilogue
-// warps add the segments in registers, rounded to nearest, while the next ones
-// run. Products whose result is rounded to bfloat16 (dW, dH of bfloat16
-// operands) are one segment: 2^-9 hides what truncation loses.
+// (1024 deep for the logits of a loss, 256 deep in every product of FP32
+// operands); the epilogue warps add the segments in registers, rounded to nearest,
+// while the next ones run. A segment's end costs the tensor cores about 600
+// cycles (4096 x 65536 x 4096: 1357 us at 512 deep, 1272 at 1024, 1215 undivided),
+// so what is rounded to bfloat16 in the end (dZ, dW, dH of bfloat16 operands) is
+// one segment: 2^-9 hides what truncation loses.
 //
 // Warps of a CTA (three warpgroups): 0 TMA producer, 1 MMA issuer (rank 0 of a
 // pair), 2 and 3 idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4) and
@@ -30,6 +37,7 @@
 // most of its own over (setmaxnreg). Ring and accumulator barriers are those of the TF32 kernel (tf32_kernels.cu): full /
 // empty per stage, acc_full / acc_empty per accumulator, all waits bounded.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -158,7 +166,12 @@ __device__ __forceinline__ int segment_blocks(const VocabTileParams &p, int kind
     return kind == kVocabDw || kind == kVocabDh ? p.seg_g : p.seg_z;
 }
 
-// Parts of A and B in product i (0..5) of the six; a call of fewer parts runs the last ones.
+__device__ __forceinline__ int product_count(const VocabTileParams &p, int kind)
+{
+    return kind == kVocabDw || kind == kVocabDh ? p.products : p.z_products;
+}
+
+// Parts of A and B in product i (0..5) of the six of three parts; fewer products are the last ones.
 __device__ __forceinline__ int part_a(int i) { return (0x001102 >> (4 * i)) & 3; }
 __device__ __forceinline__ int part_b(int i) { return (0x010120 >> (4 * i)) & 3; }
 
@@ -316,6 +329,7 @@ struct Row {
     int entry, id;   // the first target with an id of at least the tile's first column, and that id
     float q;
     float g, lse;    // dZ: the loss' gradient (0 for a masked token), log-sum-exp
+    float scale;     // of the logits, with what undoes the scaling of H's row
     bool used;
 };
 
@@ -332,7 +346,9 @@ __device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row,
 {
     Row r{};
     r.id = kNoTarget;
+    r.scale = p.scale;
     if (row >= p.T) return r;
+    if (p.z_f16) r.scale *= p.h_unscale[row];
     if (p.t.labels != nullptr) {
         const long long y = p.t.labels[row];
         r.used = y >= 0 && y < p.V;
@@ -376,6 +392,19 @@ __device__ __forceinline__ float (&columns(float (&acc)[COLS], int cb))[32]
     return reinterpret_cast<float(&)[32]>(acc[cb * 32]);
 }
 
+// Undo the scaling of W's rows (the same columns for every lane: broadcast loads).
+__device__ __forceinline__ void unscale_columns(const float *__restrict__ factor, float (&z)[COLS])
+{
+#pragma unroll
+    for (int i = 0; i < COLS; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(factor + i));
+        z[i] *= f.x;
+        z[i + 1] *= f.y;
+        z[i + 2] *= f.z;
+        z[i + 3] *= f.w;
+    }
+}
+
 // Z tile of a loss call: the softmax statistics of the thread's columns, and the logits at its targets. z = scale * acc;
 // the exponentials are powers of two, exp(z - m) = 2^(k acc - M) with k = scale log2(e) and M = k max(acc) rounded: M is
 // what the pair holds, so its rounding costs nothing.
@@ -389,7 +418,7 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     float m[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
     for (int i = 0; i < COLS; ++i) m[i & 3] = fmaxf(m[i & 3], z[i]);
-    const float k = p.scale * kLog2e, top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    const float k = r.scale * kLog2e, top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     const float base = top == -kInf ? 0.0f : -top;
     const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(base, base);
     unsigned long long s2[4] = {};
@@ -406,7 +435,7 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
         float x = 0.0f;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
-        p.zt[row * p.t.n + r.entry] = p.scale * x;
+        p.zt[row * p.t.n + r.entry] = r.scale * x;
     });
 }
 
@@ -414,7 +443,7 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
 __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
     // exp(z - lse) = 2^(k acc - L) 2^-l with L + l = lse log2(e), L rounded and l its remainder: l goes into the factor.
-    const float k = p.scale * kLog2e, L = r.lse * kLog2e;
+    const float k = r.scale * kLog2e, L = r.lse * kLog2e;
     const float l = fmaf(r.lse, kLog2e, -L) + r.lse * kLog2eLow;
     const float g = r.g * exp2_approx(-l);
     const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(-L, -L), g2 = pack_f32x2(g, g);
@@ -452,8 +481,8 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
     Item w;
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool z = w.kind == kVocabLoss || w.kind == kVocabDz;
-        const CUtensorMap *ta = z ? &maps.H : &maps.G;
-        const CUtensorMap *tb = w.kind == kVocabDw ? &maps.H : &maps.W;
+        const CUtensorMap *ta = z ? &maps.Hz : &maps.G;
+        const CUtensorMap *tb = z ? &maps.Wz : w.kind == kVocabDw ? &maps.H : &maps.W;
         const bool a_k = w.kind != kVocabDw, b_k = z;  // K-major: K along the map's rows
         const int a_r = w.m0 + static_cast<int>(rank) * 128;
         const int b_r = w.n0 + static_cast<int>(rank) * S::CTA_N + (z ? p.z_v0 : 0);
@@ -461,7 +490,7 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
         const int seg = segment_blocks(p, w.kind);
         for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg) {
             const int s1 = min(s0 + seg, w.kb1);
-            for (int pr = 6 - p.products; ok && pr < 6; ++pr) {
+            for (int pr = 6 - product_count(p, w.kind); ok && pr < 6; ++pr) {
                 const int pa = part_a(pr), pb = part_b(pr);
                 for (int kb = s0; kb < s1; ++kb) {
                     if (!mbar_wait_bounded(smem_addr(&bars->empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
@@ -536,7 +565,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
     Item w;
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool a_mn = w.kind == kVocabDw, b_mn = w.kind == kVocabDw || w.kind == kVocabDh;
-        const uint32_t idesc = idesc_bf16(S::BM, BN, a_mn, b_mn);
+        const uint32_t idesc = idesc_16(S::BM, BN, a_mn, b_mn, p.z_f16 && !b_mn);
         const int seg = segment_blocks(p, w.kind);
         for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
@@ -549,7 +578,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
             }
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * BN);
-            const int slabs = (min(s0 + seg, w.kb1) - s0) * p.products;
+            const int slabs = (min(s0 + seg, w.kb1) - s0) * product_count(p, w.kind);
             for (int j = 0; j < slabs; ++j) {
                 if (!mbar_wait_cluster_bounded(smem_addr(&bars->full[stage]), phase, abort_flag, p.timeout_ns)) {
                     raise_abort(bars, p, kTimeoutCode | kWhereMmaEmpty);
@@ -568,9 +597,9 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
                                                  : smem_desc_k_sw128(b_s + k * MMA_K * 2);
                     const uint32_t accumulate = (j | k) != 0 ? 1u : 0u;
                     if constexpr (PAIR)
-                        mma_bf16_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
+                        mma_16_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
                     else
-                        mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);
+                        mma_16(d_tmem, a_desc, b_desc, idesc, accumulate);
                 }
                 if constexpr (PAIR)
                     mma_commit_pair_both(smem_addr(&bars->empty[stage]));
@@ -658,6 +687,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             }
         }
         if (!ok) break;
+        if (p.z_f16 && (w.kind == kVocabLoss || w.kind == kVocabDz)) unscale_columns(p.w_unscale + p.z_v0 + c0, acc);
         if (w.kind == kVocabLoss) {
             leave_loss(p, acc, r, r0 + lane, p.z_v0 + c0);
             continue;
@@ -736,8 +766,8 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
         bars->abort_flag = 0;
         bars->ring_offset = a_base;
         fence_barrier_init();
-        prefetch_tensormap(&maps.H);
-        prefetch_tensormap(&maps.W);
+        prefetch_tensormap(&maps.Hz);
+        prefetch_tensormap(&maps.Wz);
         prefetch_tensormap(&maps.G);
     }
     if (warp == 0) {
@@ -788,66 +818,109 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
     }
 }
 
-// Operand of FP32 or bfloat16 at any row stride -> PARTS bfloat16 parts at a 16-byte row stride:
-// x = x0 + x1 + x2, each the remainder rounded to nearest (three parts hold all 24 bits). A value that
-// would round to infinity is truncated instead; infinities and NaN stay in the first part. 64 threads
-// per row, N neighbouring elements each: 8 where rows can be read 16 bytes at a time, else 2.
-template <typename E, int PARTS, int N>
+// bfloat16 rows at any stride -> rows at a 16-byte stride. 64 threads per row, two elements each.
 __global__ void __launch_bounds__(256)
-vocab_parts_kernel(const E *__restrict__ src, long long ld, int rows, int cols, __nv_bfloat16 *__restrict__ dst,
-                   long long ldd, long long part)
+vocab_copy_kernel(const __nv_bfloat16 *__restrict__ src, long long ld, int rows, int cols,
+                  __nv_bfloat16 *__restrict__ dst, long long ldd)
 {
     pdl_wait();
     pdl_trigger();
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (r >= rows) return;
-    const E *s = src + r * ld;
-    __nv_bfloat16 *d = dst + r * ldd;
+    const __nv_bfloat16 *s = src + r * ld;
 #pragma unroll 4
-    for (int c = threadIdx.x * N; c < ldd; c += 64 * N) {
-        alignas(16) E in[N];
-        if (N == 8 && c + N <= cols) {
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(in) / 16); ++i)
-                reinterpret_cast<uint4 *>(in)[i] = reinterpret_cast<const uint4 *>(s + c)[i];
+    for (int c = threadIdx.x * 2; c < ldd; c += 128) {
+        const __nv_bfloat16 zero = __float2bfloat16_rn(0.0f);
+        const __nv_bfloat162 y(c < cols ? __ldg(s + c) : zero, c + 1 < cols ? __ldg(s + c + 1) : zero);
+        *reinterpret_cast<__nv_bfloat162 *>(dst + r * ldd + c) = y;
+    }
+}
+
+// FP32 rows at any stride -> 16-bit parts at a 16-byte row stride, a warp per row:
+//   f16:  x 2^s = x0 + x1 in float16, s for each row such that its largest finite element lands in [2^14, 2^15);
+//         2^-s is kept. (The row is read a second time from the cache.)
+//   BF parts in bfloat16: x = x0 + x1 (+ x2), each the remainder rounded to nearest; three hold all 24 bits. A value
+//         that would round to infinity is truncated instead.
+// Infinities and NaN stay in the first part. VEC: rows can be read 16 bytes at a time.
+template <int BF, bool VEC>
+__global__ void __launch_bounds__(256)
+vocab_split_kernel(const float *__restrict__ src, long long ld, int rows, int cols, __half *__restrict__ f16,
+                   float *__restrict__ unscale, __nv_bfloat16 *__restrict__ bf, long long ldd)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x;
+    const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (r >= rows) return;
+    const float *s = src + r * ld;
+    const long long part = rows * ldd;
+    auto load = [&](int c, float (&x)[4]) {
+        if (VEC && c + 4 <= cols) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(s + c));
+            x[0] = v.x;
+            x[1] = v.y;
+            x[2] = v.z;
+            x[3] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) in[i] = c + i < cols ? s[c + i] : static_cast<E>(0.0f);
+            for (int i = 0; i < 4; ++i) x[i] = c + i < cols ? __ldg(s + c + i) : 0.0f;
         }
-        float x[N];
+    };
+    int e = 0;
+    if (f16 != nullptr) {
+        float most = 0.0f;
+#pragma unroll 4
+        for (int c = lane * 4; c < cols; c += 128) {
+            float x[4];
+            load(c, x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = static_cast<float>(in[i]);
-#pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
-            alignas(16) __nv_bfloat16 y[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                y[i] = __float2bfloat16_rn(x[i]);
-                if (PARTS > 1) {
-                    const bool fine = fabsf(x[i]) < kInf;
-                    if (fine && __hisinf(y[i])) y[i] = __float2bfloat16_rz(x[i]);
-                    x[i] = fine ? x[i] - __bfloat162float(y[i]) : 0.0f;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float a = fabsf(x[i]);
+                most = a < kInf ? fmaxf(most, a) : most;
             }
-            if constexpr (N == 8)
-                *reinterpret_cast<uint4 *>(d + k * part + c) = *reinterpret_cast<const uint4 *>(y);
-            else
-                *reinterpret_cast<uint32_t *>(d + k * part + c) = *reinterpret_cast<const uint32_t *>(y);
+        }
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        e = most > 0.0f ? 14 - ilogbf(most) : 0;
+        if (lane == 0) unscale[r] = scalbnf(1.0f, -e);
+    }
+    const float up = scalbnf(1.0f, e / 2), up2 = scalbnf(1.0f, e - e / 2);  // 2^e itself may not be an FP32 number
+#pragma unroll 4
+    for (int c = lane * 4; c < ldd; c += 128) {
+        float x[4];
+        load(c, x);
+        if (f16 != nullptr) {
+            __half y[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[i] * up * up2;
+                y[0][i] = __float2half_rn(a);
+                y[1][i] = fabsf(a) < kInf ? __float2half_rn(a - __half2float(y[0][i])) : __float2half_rn(0.0f);
+            }
+            *reinterpret_cast<uint2 *>(f16 + r * ldd + c) = *reinterpret_cast<const uint2 *>(y[0]);
+            *reinterpret_cast<uint2 *>(f16 + part + r * ldd + c) = *reinterpret_cast<const uint2 *>(y[1]);
+        }
+#pragma unroll
+        for (int k = 0; k < BF; ++k) {
+            __nv_bfloat16 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool fine = fabsf(x[i]) < kInf;
+                y[i] = __float2bfloat16_rn(x[i]);
+                if (fine && __hisinf(y[i])) y[i] = __float2bfloat16_rz(x[i]);
+                x[i] = fine ? x[i] - __bfloat162float(y[i]) : 0.0f;
+            }
+            *reinterpret_cast<uint2 *>(bf + k * part + r * ldd + c) = *reinterpret_cast<const uint2 *>(y);
         }
     }
 }
 
-template <typename E, int PARTS>
-cudaError_t launch_parts(const E *src, long long ld, int rows, int cols, __nv_bfloat16 *dst, long long ldd,
-                         long long part, bool dependent, cudaStream_t stream)
+template <int BF>
+cudaError_t launch_split(const float *src, long long ld, int rows, int cols, __half *f16, float *unscale,
+                         __nv_bfloat16 *bf, long long ldd, bool dependent, cudaStream_t stream)
 {
-    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld * sizeof(E) % 16 == 0;
-    const dim3 grid((rows + 3) / 4), block(64, 4);
-    if (vec)
-        return launch_kernel(dependent, vocab_parts_kernel<E, PARTS, 8>, grid, block, 0, stream, src, ld, rows, cols, dst,
-                             ldd, part);
-    return launch_kernel(dependent, vocab_parts_kernel<E, PARTS, 2>, grid, block, 0, stream, src, ld, rows, cols, dst, ldd,
-                         part);
+    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld % 4 == 0;
+    return launch_kernel(dependent, vec ? vocab_split_kernel<BF, true> : vocab_split_kernel<BF, false>, dim3((rows + 7) / 8),
+                         dim3(32, 8), 0, stream, src, ld, rows, cols, f16, unscale, bf, ldd);
 }
 
 template <int CTAS>
@@ -899,16 +972,22 @@ cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, 
     return launch_kernel(dependent, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, maps, p);
 }
 
-cudaError_t launch_vocab_parts(const void *src, int dtype, long long ld, int rows, int cols, int parts, void *dst,
-                               long long ldd, long long part, bool dependent, cudaStream_t stream)
+cudaError_t launch_vocab_copy(const void *src, long long ld, int rows, int cols, void *dst, long long ldd, bool dependent,
+                              cudaStream_t stream)
 {
-    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(dst);
-    if (dtype == SGEMM_DTYPE_BF16)
-        return launch_parts<__nv_bfloat16, 1>(static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, d, ldd, part,
-                                              dependent, stream);
-    const float *f = static_cast<const float *>(src);
-    return parts == 2 ? launch_parts<float, 2>(f, ld, rows, cols, d, ldd, part, dependent, stream)
-                      : launch_parts<float, 3>(f, ld, rows, cols, d, ldd, part, dependent, stream);
+    return launch_kernel(dependent, vocab_copy_kernel, dim3((rows + 3) / 4), dim3(64, 4), 0, stream,
+                         static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, static_cast<__nv_bfloat16 *>(dst), ldd);
+}
+
+cudaError_t launch_vocab_split(const void *src, long long ld, int rows, int cols, void *f16, float *unscale, void *bf,
+                               int parts, long long ldd, bool dependent, cudaStream_t stream)
+{
+    const float *s = static_cast<const float *>(src);
+    __half *f = static_cast<__half *>(f16);
+    __nv_bfloat16 *b = static_cast<__nv_bfloat16 *>(bf);
+    if (bf == nullptr) return launch_split<0>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream);
+    return parts == 2 ? launch_split<2>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream)
+                      : launch_split<3>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream);
 }
 
 }  // namespace sgemm_impl

@@ -52,25 +52,39 @@ VocabLayout vocab_layout(const VocabProblem &q)
     const bool f32 = q.dtype == SGEMM_DTYPE_F32;
     w.parts = !f32 ? 1 : q.math_mode == SGEMM_MATH_TF32 ? 2 : 3;
     w.products = w.parts * (w.parts + 1) / 2;
-    // Up to 128 tokens fill the rows of one CTA's tile: a pair would compute 128 rows of nothing.
+    // A pair's 256 rows cost less per row than a CTA's 128, but a last pair that is half empty costs the whole: the
+    // loss takes single CTAs where the tokens end in the first half of one of up to three pairs (131072 x 4096, us with
+    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494; 896
+    // and more: within 3 % of each other). Of the gradient's products only one has its rows counted in tokens, and its
+    // few tokens leave the pairs' wider tiles waiting for operands: single CTAs up to 256 tokens (711 / 757; 384 tokens
+    // 1015 / 968).
     const int pairs = q.pairs > 0 ? q.pairs : q.pairs < 0 ? 0 : q.num_sms / 2;
-    w.ctas = T > 128 && pairs > 0 ? 2 : 1;
+    const long long halves = (T + 127) / 128;
+    const bool single = grad ? T <= 256 : halves % 2 == 1 && halves <= 5;
+    w.ctas = single || pairs == 0 ? 1 : 2;
     w.workers = w.ctas == 2 ? pairs : q.num_sms;
     const int bm = 128 * w.ctas;
 
     const int few = f32 ? kFewTokensF32 : q.align_flags == 3 ? kFewTokensBf16 : kFewTokensCopied;
     w.few = !grad && T <= few;
-    w.copy_h = !w.few && (f32 || !(q.align_flags & 1));
-    w.copy_w = !w.few && (f32 || !(q.align_flags & 2));
-    w.ldh = w.ldw = round_up(q.D, 8);
-    if (w.copy_h) w.h_off = take(w.parts * T * w.ldh * 2);
-    if (w.copy_w) w.w_off = take(w.parts * static_cast<long long>(q.V) * w.ldw * 2);
+    w.split = f32 && !w.few;
+    w.copy_h = f32 ? w.split && q.dw : !w.few && !(q.align_flags & 1);
+    w.copy_w = f32 ? w.split && q.dh : !w.few && !(q.align_flags & 2);
+    w.ldp = round_up(q.D, 8);
+    if (w.copy_h) w.h_off = take(w.parts * T * w.ldp * 2);
+    if (w.copy_w) w.w_off = take(w.parts * static_cast<long long>(q.V) * w.ldp * 2);
+    if (w.split) {
+        w.hz_off = take(2 * T * w.ldp * 2);
+        w.wz_off = take(2 * static_cast<long long>(q.V) * w.ldp * 2);
+        w.hs_off = take(T * 4);
+        w.ws_off = take(round_up(q.V, kVocabBN) * 4);
+    }
     if (q.n > 0) {
         w.tid_off = take(T * q.n * 4);
         w.tq_off = take(T * q.n * 4);
         w.tlogq_off = take(T * q.n * 4);
     }
-    int launches = w.copy_h + w.copy_w + (q.n > 0);
+    int launches = (w.split ? 2 : w.copy_h + w.copy_w) + (q.n > 0);
     if (!grad) {
         w.stat_cols = w.few ? vocab_few_warps(q.T, q.num_sms) : 2 * ((q.V + kVocabBN - 1) / kVocabBN);
         w.zt_off = take(T * std::max(1, q.n) * 4);
