@@ -43,7 +43,11 @@ enum : int {
     kWhereIdxSplitReduce = 30,// split-K reduction's slice reads
     kWhereIdxTf32Copy = 33,   // TF32 TMA tile coordinate
     kWhereIdxTf32Store = 34,  // TF32 store to C or to a partial tile
-    kWhereIdxVocabDz = 35     // vocabulary losses: columns of dZ outside a piece's buffer
+    kWhereIdxVocabDz = 35,    // vocabulary losses: columns of dZ outside a piece's buffer
+    kWhereIdxVocabStat = 36,  // a (max, sum) pair outside the workspace
+    kWhereIdxVocabTarget = 37,// a target's logit outside the workspace
+    kWhereIdxVocabDw = 38,    // a row of dW outside V
+    kWhereIdxVocabDh = 39     // a split of dH outside the workspace
 };
 
 // Everything the FFMA mainloop needs besides the two tensor maps.

@@ -190,8 +190,10 @@ int run_loss(const Call &c)
     p.z_items = p.z_tm * p.z_tn;
     p.part = reinterpret_cast<float2 *>(ws + w.part_off);
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
+    p.stat_cols = w.stat_cols;
     if (w.few) {
-        const VocabFewParams f{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0};
+        const VocabFewParams f{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0,
+                               c.h->d_status};
         const bool vec = problem(c).align_flags == 3;
         if (launch_vocab_few(f, c.dtype, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
@@ -242,6 +244,7 @@ int run_grad(const Call &c)
     p.dh_tm = tm;
     p.dh_tn = tn;
     p.dh_kb = w.dh_kb;
+    p.dh_splits = w.dh_splits;
     if (c.dW != nullptr && p.dw_tma &&
         (rc = make_map(c.h, &m.dW, c.dW, c.dtype, c.D, c.V, c.lddw, 1, static_cast<long long>(c.lddw) * c.V, true)) !=
             SGEMM_OK)

@@ -164,17 +164,20 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             m = top;
             if (p.t.labels != nullptr) {
                 const long long y = p.t.labels[token];
-                if (y >= v && y < v + rows) p.zt[token] = p.scale * sums[warp][lane * R + static_cast<int>(y - v)];
+                if (y >= v && y < v + rows && index_ok(token < p.T, p.status, kWhereIdxVocabTarget))
+                    p.zt[token] = p.scale * sums[warp][lane * R + static_cast<int>(y - v)];
             } else {
                 const long long list = static_cast<long long>(token) * p.t.n;
                 for (; entry < p.t.n; ++entry) {
                     const int y = p.t.id[list + entry];
                     if (y >= v + rows) break;  // kNoTarget ends the list too
-                    p.zt[list + entry] = p.scale * sums[warp][lane * R + y - v];
+                    if (index_ok(y >= v, p.status, kWhereIdxVocabTarget))
+                        p.zt[list + entry] = p.scale * sums[warp][lane * R + y - v];
                 }
             }
         }
-        if (mine) p.part[static_cast<long long>(gw) * p.T + token] = make_float2(m, s);
+        if (mine && index_ok(gw < static_cast<int>(gridDim.x) * WARPS, p.status, kWhereIdxVocabStat))
+            p.part[static_cast<long long>(gw) * p.T + token] = make_float2(m, s);
     }
 }
 

@@ -94,6 +94,7 @@ struct VocabFewParams {
     float2 *part;  // [vocab_few_warps][T]
     float *zt;
     int rows;  // of the vocabulary per warp (set by the launch)
+    int *status;
 };
 int vocab_few_warps(int T, int num_sms);
 cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms, bool dependent, cudaStream_t stream);
@@ -115,6 +116,7 @@ struct VocabTileParams {
     int z_items;
     float2 *part;
     float *zt;
+    int stat_cols;       // pairs per token at part
     const float *lse, *dloss;
     int g_blocks;        // dZ's buffer: blocks of 64 entries per part, [parts][g_blocks][T][64]
     // dH and dW tiles of the piece [g_v0, g_v0 + g_vn), whose dZ an earlier launch left
@@ -125,7 +127,7 @@ struct VocabTileParams {
     long long lddw;
     bool dw_tma, dw_vec;  // dW is written by TMA stores; else whether 4 elements of a row at a time
     float alpha, beta;    // dH = alpha * G W (summed over the pieces), dW = alpha * G^T H + beta * dW, alpha = c * scale
-    int dh_tm, dh_tn, dh_kb;
+    int dh_tm, dh_tn, dh_kb, dh_splits;
     int dh_items;
     int dh_extra;  // other tiles for a worker that has one dH tile fewer
     bool acc_add;  // dH: add to the sums (a later piece)

@@ -430,12 +430,14 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     }
     float x, y;
     unpack_f32x2(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), x, y);
-    if (row < p.T) p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(top, x + y);
+    if (row < p.T && index_ok(c0 / COLS < p.stat_cols, p.status, kWhereIdxVocabStat))
+        p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(top, x + y);
     for_targets(p, r, row, c0, [&](int at) {
         float x = 0.0f;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
-        p.zt[row * p.t.n + r.entry] = r.scale * x;
+        if (index_ok(row < p.T && r.entry >= 0 && r.entry < p.t.n, p.status, kWhereIdxVocabTarget))
+            p.zt[row * p.t.n + r.entry] = r.scale * x;
     });
 }
 
@@ -706,9 +708,10 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             inside = inside && index_ok(c0 + COLS <= cols, p.status, kWhereIdxVocabDz);
         } else if (w.kind == kVocabDh) {
             map = &maps.acc;
+            inside = inside && index_ok(w.split >= 0 && w.split < p.dh_splits, p.status, kWhereIdxVocabDh);
         } else {
             row = p.g_v0 + r0;
-            inside = r0 < p.g_vn;
+            inside = r0 < p.g_vn && index_ok(row < p.V && p.g_v0 + p.g_vn <= p.V, p.status, kWhereIdxVocabDw);
         }
         if (!inside) continue;
         if (w.kind == kVocabDw && !p.dw_tma) {

@@ -14,8 +14,8 @@ namespace {
 constexpr long long kPieceBytes = 256LL << 20;
 
 // Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
-// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 69 / 345, 24
-// tokens 263 / 345, 32 tokens 350 / 345; bfloat16 131072 x 4096, 2 tokens 158 / 178, 3 tokens 233 / 177; rows at an odd
+// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 82 / 279, 24
+// tokens 230 / 278, 32 tokens 301 / 278; bfloat16 131072 x 4096, 2 tokens 158 / 178, 3 tokens 233 / 177; rows at an odd
 // stride, 50021 x 1531, 8 tokens 86 / 92.
 constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
 
@@ -54,8 +54,8 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.products = w.parts * (w.parts + 1) / 2;
     // A pair's 256 rows cost less per row than a CTA's 128, but a last pair that is half empty costs the whole: the
     // loss takes single CTAs where the tokens end in the first half of one of up to three pairs (131072 x 4096, us with
-    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494; 896
-    // and more: within 3 % of each other). Of the gradient's products only one has its rows counted in tokens, and its
+    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494; 768 tokens
+    // 524 / 508). Of the gradient's products only one has its rows counted in tokens, and its
     // few tokens leave the pairs' wider tiles waiting for operands: single CTAs up to 256 tokens (711 / 757; 384 tokens
     // 1015 / 968).
     const int pairs = q.pairs > 0 ? q.pairs : q.pairs < 0 ? 0 : q.num_sms / 2;

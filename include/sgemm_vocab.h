@@ -51,12 +51,19 @@
  * Numerics: loss and lse are FP32 whatever the operands' type; products are
  * accumulated in FP32, softmax statistics are kept in FP32. bfloat16 operands
  * enter the products as they are and dZ enters them rounded to bfloat16; dH and
- * dW are rounded once. FP32 operands enter as sums of bfloat16 parts: three parts
- * (24 bits, the products down to 2^-16 of the leading one) by default, two parts
- * with SGEMM_MATH_TF32. dZ is split likewise. Results are bitwise reproducible for
- * a fixed shape, alignment and plan.
+ * dW are rounded once. FP32 operands enter the tensor cores as sums of 16-bit
+ * parts: for the logits two float16 parts (22 bits) of rows scaled by powers of
+ * two, for dH and dW, with dZ split likewise, three bfloat16 parts (24 bits; two
+ * parts with SGEMM_MATH_TF32). Results are bitwise reproducible for a fixed shape,
+ * alignment and plan.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.
+ * T, V or D so large that their tiles do not count in 32 bits: SGEMM_ERR_NOT_SUPPORTED.
+ * Device status (sgemm_check_device_status): the TF32 kernel's locations; in debug
+ * builds also 35 the columns of dZ, 36 the softmax statistics, 37 the targets'
+ * logits, 38 the rows of dW, 39 the splits of dH.
+ *
+ * CUDA graphs: as sgemm_run, once the workspace holds the plan's workspace_bytes.
  */
 #ifndef SGEMM_GB300_VOCAB_H
 #define SGEMM_GB300_VOCAB_H
