@@ -92,32 +92,36 @@ int make_map(sgemm_handle_t h, CUtensorMap *map, const void *base, int dtype, in
     return r == CUDA_SUCCESS ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
 
-// The maps of H or W, as Z reads it and as the other products do: the caller's matrix, or what is first made of it in
-// the workspace.
+// The map of a bfloat16 operand: the caller's matrix, or an aligned copy of it, which is made first.
 int map_operand(const Call &c, const VocabLayout &w, bool copy, const void *src, int rows, int ld, long long off,
-                long long z_off, float *unscale, CUtensorMap *z_map, CUtensorMap *map)
+                CUtensorMap *map)
+{
+    if (!copy) return make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
+    void *dst = static_cast<char *>(c.h->workspace) + off;
+    if (launch_vocab_copy(src, ld, rows, c.D, dst, w.ldp, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    return make_map(c.h, map, dst, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, 1, rows * w.ldp, false);
+}
+
+// FP32 operands as parts: H (float16, and bfloat16 where dW reads it), then W (float16).
+int split_operands(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
 {
     char *ws = static_cast<char *>(c.h->workspace);
-    const long long part = rows * w.ldp;
-    int rc = SGEMM_OK;
-    if (w.split) {
-        if (launch_vocab_split(src, ld, rows, c.D, ws + z_off, unscale, copy ? ws + off : nullptr, w.parts, w.ldp,
-                               c.dependent(), c.stream) != cudaSuccess)
-            return SGEMM_ERR_LAUNCH;
-        rc = make_map(c.h, z_map, ws + z_off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, 2, part, false);
-        *map = *z_map;
-        if (rc == SGEMM_OK && copy)
-            rc = make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, w.parts, part, false);
-        return rc;
-    }
-    if (copy) {
-        if (launch_vocab_copy(src, ld, rows, c.D, ws + off, w.ldp, c.dependent(), c.stream) != cudaSuccess)
-            return SGEMM_ERR_LAUNCH;
-        rc = make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, c.D, rows, w.ldp, 1, part, false);
-    } else {
-        rc = make_map(c.h, map, src, SGEMM_DTYPE_BF16, c.D, rows, ld, 1, static_cast<long long>(ld) * rows, false);
-    }
-    *z_map = *map;
+    float *hs = reinterpret_cast<float *>(ws + w.hs_off), *most = reinterpret_cast<float *>(ws + w.ws_off), *vs = most + 64;
+    const int padded = (c.V + kVocabBN - 1) / kVocabBN * kVocabBN;
+    const long long h_part = c.T * w.ldp, w_part = c.V * w.ldp;
+    if (launch_vocab_split(c.H, c.ldh, c.T, c.D, ws + w.hz_off, hs, c.T, nullptr, most, w.copy_h ? ws + w.h_off : nullptr,
+                           w.parts, w.ldp, c.dependent(), c.stream) != cudaSuccess ||
+        launch_vocab_split(c.W, c.ldw, c.V, c.D, ws + w.wz_off, vs, padded, most, nullptr, nullptr, 0, w.ldp, c.dependent(),
+                           c.stream) != cudaSuccess)
+        return SGEMM_ERR_LAUNCH;
+    p->h_unscale = hs;
+    p->w_unscale = vs;
+    p->w_most = most;
+    int rc = make_map(c.h, &m->Hz, ws + w.hz_off, SGEMM_DTYPE_BF16, c.D, c.T, w.ldp, 2, h_part, false);
+    if (rc == SGEMM_OK) rc = make_map(c.h, &m->W, ws + w.wz_off, SGEMM_DTYPE_BF16, c.D, c.V, w.ldp, 2, w_part, false);
+    m->H = m->Hz;
+    if (rc == SGEMM_OK && w.copy_h)
+        rc = make_map(c.h, &m->H, ws + w.h_off, SGEMM_DTYPE_BF16, c.D, c.T, w.ldp, w.parts, h_part, false);
     return rc;
 }
 
@@ -126,16 +130,17 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
 {
     char *ws = static_cast<char *>(c.h->workspace);
     if (!w.few) {
-        float *hs = reinterpret_cast<float *>(ws + w.hs_off), *vs = reinterpret_cast<float *>(ws + w.ws_off);
         int rc;
-        if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, w.hz_off, hs, &m->Hz, &m->H)) != SGEMM_OK)
-            return rc;
-        if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, w.wz_off, vs, &m->Wz, &m->W)) != SGEMM_OK)
-            return rc;
-        m->G = m->Gw = m->acc = m->dW = m->W;  // where a call has no such matrix, a valid map that no tile uses
-        p->z_f16 = w.split;
-        p->h_unscale = hs;
-        p->w_unscale = vs;
+        if (w.split) {
+            if ((rc = split_operands(c, w, p, m)) != SGEMM_OK) return rc;
+        } else {
+            if ((rc = map_operand(c, w, w.copy_h, c.H, c.T, c.ldh, w.h_off, &m->H)) != SGEMM_OK) return rc;
+            if ((rc = map_operand(c, w, w.copy_w, c.W, c.V, c.ldw, w.w_off, &m->W)) != SGEMM_OK) return rc;
+            m->Hz = m->H;
+        }
+        // where a call has no such matrix, a valid map that no tile uses
+        m->G = m->Gz = m->Gw = m->Gzw = m->acc = m->dW = m->W;
+        p->f16 = w.split;
     }
     p->T = c.T;
     p->V = c.V;
@@ -143,12 +148,12 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     p->dtype = c.dtype;
     p->parts = w.parts;
     p->products = w.products;
-    p->z_products = w.split ? 3 : 1;
+    p->f16_products = w.split ? 3 : 1;
     // Segments (vocab_kernels.cu): 1024 deep for the logits of a loss, 256 for FP32 operands, whole for what is rounded
     // to bfloat16.
     const int whole = 1 << 24;
-    p->seg_z = w.parts > 1 ? 4 : c.dH == nullptr && c.dW == nullptr ? 16 : whole;
-    p->seg_g = w.parts > 1 ? 4 : whole;
+    p->seg_z = w.split ? 4 : c.dH == nullptr && c.dW == nullptr ? 16 : whole;
+    p->seg_g = w.split ? 4 : whole;
     p->scale = c.scale;
     p->lse = c.lse;
     p->dloss = c.dloss;
@@ -230,8 +235,16 @@ int run_grad(const Call &c)
     p.g_blocks = w.g_blocks;
     const long long acc_split = c.T * w.ldacc;
     // dZ in blocks of 64 entries, T x 64 each: every copy of it is one contiguous piece of memory
-    auto dz_map = [&](CUtensorMap *map, long long off, bool result) {
-        return make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, 64, c.T, 64, w.parts * w.g_blocks, 64LL * c.T, result);
+    auto dz_map = [&](CUtensorMap *map, long long off, int parts, bool result) {
+        return make_map(c.h, map, ws + off, SGEMM_DTYPE_BF16, 64, c.T, 64, parts * w.g_blocks, 64LL * c.T, result);
+    };
+    // as dW and as dH read it: the same for bfloat16 operands
+    auto dz_maps = [&](CUtensorMap *map, CUtensorMap *map_dh, int i, bool result) {
+        int e = SGEMM_OK;
+        if (!w.split || c.dW != nullptr) e = dz_map(map, w.g_off[i], w.parts, result);
+        *map_dh = *map;
+        if (e == SGEMM_OK && w.split && c.dH != nullptr) e = dz_map(map_dh, w.gz_off[i], 2, result);
+        return e;
     };
     float *acc = reinterpret_cast<float *>(ws + w.acc_off);
     p.dW = c.dW;
@@ -240,8 +253,8 @@ int run_grad(const Call &c)
     p.dw_vec = aligned(c.dW, 4 * elem) && c.lddw % 4 == 0;
     p.alpha = c.mult * c.scale;
     p.beta = c.beta;
-    p.dw_tn = tn;
-    p.dh_tm = tm;
+    p.dw_tn = c.dW != nullptr ? tn : 0;  // 0: no such gradient
+    p.dh_tm = c.dH != nullptr ? tm : 0;
     p.dh_tn = tn;
     p.dh_kb = w.dh_kb;
     p.dh_splits = w.dh_splits;
@@ -262,17 +275,18 @@ int run_grad(const Call &c)
             if (c.dH != nullptr) p.dh_items = tm * tn * splits;
             if (c.dW != nullptr) p.dw_items = ceil_div(p.g_vn, bm) * tn;
             p.acc_add = i > 1;
-            if ((rc = dz_map(&m.G, w.g_off[(i - 1) & 1], false)) != SGEMM_OK) return rc;
+            if ((rc = dz_maps(&m.G, &m.Gz, (i - 1) & 1, false)) != SGEMM_OK) return rc;
         }
         if (i < w.pub.pieces) {
             p.z_v0 = i * w.pub.piece;
             p.z_tn = ceil_div(c.V - p.z_v0 < w.pub.piece ? c.V - p.z_v0 : w.pub.piece, kVocabBN);
             p.z_items = tm * p.z_tn;
-            if ((rc = dz_map(&m.Gw, w.g_off[i & 1], true)) != SGEMM_OK) return rc;
+            if ((rc = dz_maps(&m.Gw, &m.Gzw, i & 1, true)) != SGEMM_OK) return rc;
         }
         const int others = p.dw_items + p.z_items, rem = p.dh_items % w.workers;
         const int cost = vocab_cost(c.dW != nullptr ? c.T : c.D);
-        p.dh_extra = p.dh_items > 0 && rem > 0 ? std::min((w.dh_kb + cost / 2) / cost, others / (w.workers - rem)) : 0;
+        const int own = w.products == 6 && c.dW != nullptr ? w.dh_kb / 2 : w.dh_kb;  // a k-block of dW has twice the products
+        p.dh_extra = p.dh_items > 0 && rem > 0 ? std::min((own + cost / 2) / cost, others / (w.workers - rem)) : 0;
         if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     }
     if (c.dH != nullptr && launch_vocab_finish(c.T, c.D, acc, w.ldacc, acc_split, w.dh_splits, c.beta, c.dH, c.lddh,

@@ -47,13 +47,14 @@ struct VocabLayout {
     bool few;      // a few tokens: vocab_few.cu, no parts
     int ctas;      // CTAs per worker: 2 = pairs computing 256 x 256 tiles, 1 = 128 x 256
     int workers;
-    int parts, products;  // bfloat16 parts of dZ and of the operands of dH and dW, products of parts
     bool split;           // FP32 operands, used as 16-bit parts
-    bool copy_h, copy_w;  // workspace rows of H and W: an aligned copy, or bfloat16 parts
+    int parts, products;  // parts of dZ and of the operands of dW, products of parts
+    bool copy_h, copy_w;  // workspace rows of H and W: an aligned copy; of a split H, bfloat16 parts for dW
     long long ldp;                         // elements of such a row
     long long h_off, w_off;                // [parts][rows][ldp]
-    long long hz_off, wz_off;              // float16 parts for Z, [2][rows][ldp]
-    long long hs_off, ws_off;              // what undoes their rows' scaling; W's in whole tiles
+    long long hz_off, wz_off;              // float16 parts, [2][rows][ldp]
+    long long hs_off, ws_off;              // what undoes their rows' scaling; W's in whole tiles, after the largest of it
+    long long gz_off[2];                   // dZ of a piece in float16 parts for dH, [2][g_blocks][T][64]
     long long tid_off, tq_off, tlogq_off;  // target tables [T][n]
     long long zt_off;                      // logits at the targets, [T][n]
     long long part_off;                    // (max, sum of exp) per token and 128 columns or warp, [stat_cols][T]
@@ -105,9 +106,10 @@ enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };
 struct VocabTileParams {
     int T, V, D;
     int dtype;
-    int parts, products, z_products;
-    bool z_f16;  // Z's operands are float16 parts, scaled row by row
-    const float *h_unscale, *w_unscale;
+    int parts, products;  // of dW
+    bool f16;             // FP32 operands: those of Z and dH are float16 parts, scaled row by row
+    int f16_products;     // of Z and dH (1 for bfloat16 operands)
+    const float *h_unscale, *w_unscale, *w_most;
     int seg_z, seg_g;  // k-blocks per accumulator segment
     float scale;
     VocabTargets t;
@@ -136,18 +138,19 @@ struct VocabTileParams {
 };
 cudaError_t vocab_set_attributes();
 int vocab_max_pairs();
-// Maps (elements of a row, rows, parts), all with the 128-byte swizzle: operands in boxes of 64 x 64 x 1 (H and W
-// as Z reads them and as dW and dH do, the piece's dZ G), results in boxes of 128 bytes x 32 rows (dZ written, the sums of dH by split, dW where dw_tma).
+// Maps (elements of a row, rows, parts), all with the 128-byte swizzle: operands in boxes of 64 x 64 x 1 (H as Z
+// and as dW read it, W, the piece's dZ as dW and as dH read it), results in boxes of 128 bytes x 32 rows (dZ written, twice, the sums of dH by split, dW where dw_tma).
 struct VocabMaps {
-    CUtensorMap Hz, Wz, H, W, G, Gw, acc, dW;
+    CUtensorMap Hz, H, W, G, Gz, Gw, Gzw, acc, dW;
 };
 cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, int ctas, int workers, bool dependent,
                                cudaStream_t stream);
-// bfloat16 rows copied to a row stride of ldd; FP32 rows split into two float16 parts (f16, with what undoes each row's
-// scaling) and / or bfloat16 parts, each part rows x ldd.
+// bfloat16 rows copied to a row stride of ldd; FP32 rows split into two float16 parts (with what undoes each row's
+// scaling) and, where bf is given, bfloat16 parts, each part rows x ldd.
 cudaError_t launch_vocab_copy(const void *src, long long ld, int rows, int cols, void *dst, long long ldd, bool dependent,
                               cudaStream_t stream);
-cudaError_t launch_vocab_split(const void *src, long long ld, int rows, int cols, void *f16, float *unscale, void *bf,
-                               int parts, long long ldd, bool dependent, cudaStream_t stream);
+cudaError_t launch_vocab_split(const void *src, long long ld, int rows, int cols, void *f16, float *unscale, int padded,
+                               float *most, float *clear, void *bf, int parts, long long ldd, bool dependent,
+                               cudaStream_t stream);
 
 }  // namespace sgemm_impl

@@ -13,11 +13,11 @@
 //
 // FP32 operands (vocab_split_kernel) are sums of 16-bit parts, a product of them
 // the products of parts down to about 2^-22 of the leading one, small ones first:
-// the same loop over more slabs. For Z, whose operands are rows with one scale
-// each, two float16 parts (22 bits) of the rows scaled by powers of two, 3
-// products; an element far below its row's largest has fewer bits, but in the sum
-// it stands next to the largest. For dH and dW, where dZ spans many orders of
-// magnitude and each row of dW may be made of small ones alone, three bfloat16
+// the same loop over more slabs. For Z and dH two float16 parts (22 bits) of rows
+// scaled by powers of two, 3 products: an element far below its row's largest has
+// fewer bits, but in the sum it stands next to the largest (for dH, dZ carries
+// back the scaling of W's rows, the sum's index). For dW, where dZ spans many
+// orders of magnitude and a row may be made of small ones alone, three bfloat16
 // parts (24 bits at any magnitude), 6 products.
 //
 // Accumulation: the tensor core truncates its FP32 accumulator at every K = 16
@@ -168,7 +168,7 @@ __device__ __forceinline__ int segment_blocks(const VocabTileParams &p, int kind
 
 __device__ __forceinline__ int product_count(const VocabTileParams &p, int kind)
 {
-    return kind == kVocabDw || kind == kVocabDh ? p.products : p.z_products;
+    return kind == kVocabDw ? p.products : p.f16_products;
 }
 
 // Parts of A and B in product i (0..5) of the six of three parts; fewer products are the last ones.
@@ -269,6 +269,40 @@ __device__ __forceinline__ void send_bf16(const CUtensorMap *map, float (&acc)[C
     }
 }
 
+// dZ for dH as two float16 parts, in blocks of 64 columns: columns times 2^15 factor[column] / most, which undoes the
+// scaling of W's row against the largest such factor, so that nothing leaves float16's range (dZ is at most 1 here).
+__device__ __forceinline__ void send_f16(const CUtensorMap *map, const float (&acc)[COLS],
+                                         const float *__restrict__ factor, float most, uint32_t stg, int lane, int x, int y,
+                                         int blocks)
+{
+    const float up = 1.0f / most;  // a power of two
+#pragma unroll
+    for (int cb = 0; cb < COLS / 64; ++cb) {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float *f = acc + cb * 64 + 8 * j + 2 * i;
+                    const float2 u = __ldg(reinterpret_cast<const float2 *>(factor + cb * 64 + 8 * j + 2 * i));
+                    const float a = f[0] * (u.x * up * 32768.0f), b = f[1] * (u.y * up * 32768.0f);
+                    __half2 y2 = __floats2half2_rn(a, b);
+                    if (part == 1) {
+                        const float2 back = __half22float2(y2);
+                        y2 = __floats2half2_rn(a - back.x, b - back.y);
+                    }
+                    v[i] = *reinterpret_cast<const uint32_t *>(&y2);
+                }
+                sts128(stg + lane * 128 + ((j ^ (lane & 7)) << 4), v);
+            }
+            stage_send(map, stg, lane, 0, y, part * blocks + x / 64 + cb, false);
+        }
+    }
+}
+
 // Rows that a TMA store cannot write (not 16-byte aligned), or that are added to (beta != 0), element by element or
 // four at a time: 32 columns of FP32 staged, element (r, c) at 32 r + (c ^ r), then read back along rows.
 template <typename E>
@@ -342,13 +376,14 @@ __device__ __forceinline__ void load_target(const VocabTileParams &p, Row &r, lo
     }
 }
 
+template <bool F16>
 __device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row, int c0, bool dz)
 {
     Row r{};
     r.id = kNoTarget;
     r.scale = p.scale;
     if (row >= p.T) return r;
-    if (p.z_f16) r.scale *= p.h_unscale[row];
+    if (F16) r.scale *= p.h_unscale[row];
     if (p.t.labels != nullptr) {
         const long long y = p.t.labels[row];
         r.used = y >= 0 && y < p.V;
@@ -372,6 +407,15 @@ __device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row,
         r.lse = p.lse[row];
     }
     return r;
+}
+
+// dloss of a token, 0 for a masked one.
+__device__ __forceinline__ float load_dloss(const VocabTileParams &p, long long row)
+{
+    if (row >= p.T) return 0.0f;
+    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
+    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
+    return used ? p.dloss[row] : 0.0f;
 }
 
 // f(column - c0) for the row's targets in [c0, c0 + 128) one after the other; r.entry and r.q are the target's.
@@ -441,13 +485,15 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     });
 }
 
-// Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q).
+// Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q); for float16
+// parts without dloss, which the sums over the vocabulary and the bfloat16 parts are multiplied by instead.
+template <bool F16>
 __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
     // exp(z - lse) = 2^(k acc - L) 2^-l with L + l = lse log2(e), L rounded and l its remainder: l goes into the factor.
     const float k = r.scale * kLog2e, L = r.lse * kLog2e;
     const float l = fmaf(r.lse, kLog2e, -L) + r.lse * kLog2eLow;
-    const float g = r.g * exp2_approx(-l);
+    const float weight = F16 ? 1.0f : r.g, g = weight * exp2_approx(-l);
     const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(-L, -L), g2 = pack_f32x2(g, g);
 #pragma unroll
     for (int i = 0; i < COLS; i += 2) {
@@ -462,7 +508,7 @@ __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COL
         for (int i = 0; i < COLS; ++i) z[i] = i < cols ? z[i] : 0.0f;
     }
     for_targets(p, r, row, c0, [&](int at) {
-        const float t = r.g * r.q;
+        const float t = weight * r.q;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) z[i] -= i == at ? t : 0.0f;
     });
@@ -483,8 +529,8 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
     Item w;
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool z = w.kind == kVocabLoss || w.kind == kVocabDz;
-        const CUtensorMap *ta = z ? &maps.Hz : &maps.G;
-        const CUtensorMap *tb = z ? &maps.Wz : w.kind == kVocabDw ? &maps.H : &maps.W;
+        const CUtensorMap *ta = z ? &maps.Hz : w.kind == kVocabDw ? &maps.G : &maps.Gz;
+        const CUtensorMap *tb = w.kind == kVocabDw ? &maps.H : &maps.W;
         const bool a_k = w.kind != kVocabDw, b_k = z;  // K-major: K along the map's rows
         const int a_r = w.m0 + static_cast<int>(rank) * 128;
         const int b_r = w.n0 + static_cast<int>(rank) * S::CTA_N + (z ? p.z_v0 : 0);
@@ -552,7 +598,7 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
 }
 
 // MMA thread (rank 0 of a pair): four K = 16 steps per slab, a commit per stage and per segment.
-template <int CTAS>
+template <int CTAS, bool F16>
 __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars, uint32_t a_base,
                                       uint32_t b_base, uint32_t tmem, int worker, int workers)
 {
@@ -567,7 +613,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
     Item w;
     for (int i = 0; ok && item_at(p, i, worker, workers, S::BM, w); ++i) {
         const bool a_mn = w.kind == kVocabDw, b_mn = w.kind == kVocabDw || w.kind == kVocabDh;
-        const uint32_t idesc = idesc_16(S::BM, BN, a_mn, b_mn, p.z_f16 && !b_mn);
+        const uint32_t idesc = idesc_16(S::BM, BN, a_mn, b_mn, F16 && w.kind != kVocabDw);
         const int seg = segment_blocks(p, w.kind);
         for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
@@ -628,7 +674,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
 }
 
 // Epilogue warp: the segments of a tile added up in registers, then the tile left as its kind wants it.
-template <int CTAS>
+template <int CTAS, bool F16>
 __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape<CTAS>::STAGES> *bars,
                                             unsigned char *staging, const VocabMaps &maps, uint32_t tmem, uint32_t rank,
                                             int warp, int lane, int worker, int workers)
@@ -648,7 +694,10 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         const int r0 = w.m0 + static_cast<int>(rank) * 128 + quarter * 32;  // the warp's first row
         const int c0 = w.n0 + half * COLS;
         Row r{};
-        if (w.kind == kVocabLoss || w.kind == kVocabDz) r = load_row(p, r0 + lane, p.z_v0 + c0, w.kind == kVocabDz);
+        if (w.kind == kVocabLoss || w.kind == kVocabDz)
+            r = load_row<F16>(p, r0 + lane, p.z_v0 + c0, w.kind == kVocabDz);
+        else if (F16 && w.kind == kVocabDh)
+            r.g = load_dloss(p, r0 + lane);
         for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
@@ -689,7 +738,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             }
         }
         if (!ok) break;
-        if (p.z_f16 && (w.kind == kVocabLoss || w.kind == kVocabDz)) unscale_columns(p.w_unscale + p.z_v0 + c0, acc);
+        if (F16 && (w.kind == kVocabLoss || w.kind == kVocabDz)) unscale_columns(p.w_unscale + p.z_v0 + c0, acc);
         if (w.kind == kVocabLoss) {
             leave_loss(p, acc, r, r0 + lane, p.z_v0 + c0);
             continue;
@@ -698,16 +747,26 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         const CUtensorMap *map = &maps.dW;
         const bool wide = w.kind == kVocabDh || (w.kind == kVocabDw && p.dtype == SGEMM_DTYPE_F32);
         int row = r0, cols = p.D, parts = 1, blocks = 0;
+        float alpha = p.alpha;
         bool inside = r0 < p.T;
         if (w.kind == kVocabDz) {
-            make_dz(p, acc, r, r0 + lane, p.z_v0 + c0);
+            make_dz<F16>(p, acc, r, r0 + lane, p.z_v0 + c0);
             map = &maps.Gw;
             cols = p.g_blocks * 64;
-            parts = p.parts;
+            parts = F16 ? p.parts : 1;
             blocks = p.g_blocks;
+            alpha = 1.0f;
             inside = inside && index_ok(c0 + COLS <= cols, p.status, kWhereIdxVocabDz);
+            if (F16 && inside) {
+                if (p.dh_tm > 0)
+                    send_f16(&maps.Gzw, acc, p.w_unscale + p.z_v0 + c0, __ldg(p.w_most), stg, lane, c0, row, blocks);
+                if (p.dw_tn == 0) continue;
+#pragma unroll
+                for (int i = 0; i < COLS; ++i) acc[i] *= r.g;
+            }
         } else if (w.kind == kVocabDh) {
             map = &maps.acc;
+            if (F16) alpha *= r.g * __ldg(p.w_most) * (1.0f / 32768.0f);
             inside = inside && index_ok(w.split >= 0 && w.split < p.dh_splits, p.status, kWhereIdxVocabDh);
         } else {
             row = p.g_v0 + r0;
@@ -723,15 +782,17 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
                 write_rows(acc, reinterpret_cast<float *>(area), lane, static_cast<__nv_bfloat16 *>(p.dW) + at, p.lddw,
                            p.g_vn - r0, p.D - c0, p.dw_vec, p.alpha, p.beta);
         } else if (wide) {
-            send_f32(map, acc, stg, lane, c0, row, w.split, cols, w.kind == kVocabDh && p.acc_add, p.alpha);
+            send_f32(map, acc, stg, lane, c0, row, w.split, cols, w.kind == kVocabDh && p.acc_add, alpha);
         } else {
-            send_bf16(map, acc, stg, lane, c0, row, cols, parts, blocks, w.kind == kVocabDz ? 1.0f : p.alpha);
+            send_bf16(map, acc, stg, lane, c0, row, cols, parts, blocks, alpha);
         }
     }
     if (lane == 0) bulk_wait();  // the staging area is read and everything is written before the CTA ends
 }
 
-template <int CTAS>
+// F16: FP32 operands, whose Z and dH run on float16 parts (a kernel of its own: the code of the parts costs the other
+// 2 %).
+template <int CTAS, bool F16>
 __global__ void __launch_bounds__(THREADS, 1)
 vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabTileParams p)
 {
@@ -770,7 +831,7 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
         bars->ring_offset = a_base;
         fence_barrier_init();
         prefetch_tensormap(&maps.Hz);
-        prefetch_tensormap(&maps.Wz);
+        prefetch_tensormap(&maps.W);
         prefetch_tensormap(&maps.G);
     }
     if (warp == 0) {
@@ -802,10 +863,10 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
         if (same_layout && warp == 0 && lane == 0)
             produce<CTAS>(p, bars, a_base, b_base, maps, rank, worker, workers);
         else if (same_layout && warp == 1 && lane == 0 && rank == 0)
-            issue<CTAS>(p, bars, a_base, b_base, tmem, worker, workers);
+            issue<CTAS, F16>(p, bars, a_base, b_base, tmem, worker, workers);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPILOGUE));
-        if (same_layout) leave_tiles<CTAS>(p, bars, staging, maps, tmem, rank, warp, lane, worker, workers);
+        if (same_layout) leave_tiles<CTAS, F16>(p, bars, staging, maps, tmem, rank, warp, lane, worker, workers);
     }
 
     tc_fence_before_sync();
@@ -841,20 +902,26 @@ vocab_copy_kernel(const __nv_bfloat16 *__restrict__ src, long long ld, int rows,
 
 // FP32 rows at any stride -> 16-bit parts at a 16-byte row stride, a warp per row:
 //   f16:  x 2^s = x0 + x1 in float16, s for each row such that its largest finite element lands in [2^14, 2^15);
-//         2^-s is kept. (The row is read a second time from the cache.)
+//         2^-s is kept (2^-126 for rows without such an element and for those up to `padded`), and the largest of
+//         them in *most; *clear is the next such word to set to 0. (The row is read a second time from the cache.)
 //   BF parts in bfloat16: x = x0 + x1 (+ x2), each the remainder rounded to nearest; three hold all 24 bits. A value
 //         that would round to infinity is truncated instead.
 // Infinities and NaN stay in the first part. VEC: rows can be read 16 bytes at a time.
 template <int BF, bool VEC>
 __global__ void __launch_bounds__(256)
 vocab_split_kernel(const float *__restrict__ src, long long ld, int rows, int cols, __half *__restrict__ f16,
-                   float *__restrict__ unscale, __nv_bfloat16 *__restrict__ bf, long long ldd)
+                   float *__restrict__ unscale, int padded, float *__restrict__ most_scale, float *__restrict__ clear,
+                   __nv_bfloat16 *__restrict__ bf, long long ldd)
 {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x;
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (r >= rows) return;
+    if (clear != nullptr && r == 0 && lane == 0) *clear = 0.0f;
+    if (r >= rows) {
+        if (r < padded && lane == 0) unscale[r] = scalbnf(1.0f, -126);
+        return;
+    }
     const float *s = src + r * ld;
     const long long part = rows * ldd;
     auto load = [&](int c, float (&x)[4]) {
@@ -883,8 +950,14 @@ vocab_split_kernel(const float *__restrict__ src, long long ld, int rows, int co
             }
         }
         for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        e = most > 0.0f ? 14 - ilogbf(most) : 0;
-        if (lane == 0) unscale[r] = scalbnf(1.0f, -e);
+        e = most > 0.0f ? min(14 - ilogbf(most), 126) : 126;
+        if (lane == 0) {
+            const float back = scalbnf(1.0f, -e);
+            unscale[r] = back;
+            // positive FP32 numbers are ordered as their bits are; nearly all rows see that they add nothing
+            if (most_scale != nullptr && back > *static_cast<volatile float *>(most_scale))
+                atomicMax(reinterpret_cast<int *>(most_scale), __float_as_int(back));
+        }
     }
     const float up = scalbnf(1.0f, e / 2), up2 = scalbnf(1.0f, e - e / 2);  // 2^e itself may not be an FP32 number
 #pragma unroll 4
@@ -918,30 +991,33 @@ vocab_split_kernel(const float *__restrict__ src, long long ld, int rows, int co
 }
 
 template <int BF>
-cudaError_t launch_split(const float *src, long long ld, int rows, int cols, __half *f16, float *unscale,
-                         __nv_bfloat16 *bf, long long ldd, bool dependent, cudaStream_t stream)
+cudaError_t launch_split(const float *src, long long ld, int rows, int cols, __half *f16, float *unscale, int padded,
+                         float *most, float *clear, __nv_bfloat16 *bf, long long ldd, bool dependent,
+                         cudaStream_t stream)
 {
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld % 4 == 0;
-    return launch_kernel(dependent, vec ? vocab_split_kernel<BF, true> : vocab_split_kernel<BF, false>, dim3((rows + 7) / 8),
-                         dim3(32, 8), 0, stream, src, ld, rows, cols, f16, unscale, bf, ldd);
+    return launch_kernel(dependent, vec ? vocab_split_kernel<BF, true> : vocab_split_kernel<BF, false>, dim3((padded + 7) / 8),
+                         dim3(32, 8), 0, stream, src, ld, rows, cols, f16, unscale, padded, most, clear, bf, ldd);
 }
 
-template <int CTAS>
+template <int CTAS, bool F16>
 cudaError_t set_attributes()
 {
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, vocab_kernel<CTAS>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, vocab_kernel<CTAS, F16>);
     if (e != cudaSuccess) return e;
     if (a.numRegs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;  // the exchange of registers could not end
-    return cudaFuncSetAttribute(vocab_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CTAS>::SMEM);
+    return cudaFuncSetAttribute(vocab_kernel<CTAS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CTAS>::SMEM);
 }
 
 }  // namespace
 
 cudaError_t vocab_set_attributes()
 {
-    const cudaError_t e = set_attributes<1>();
-    return e != cudaSuccess ? e : set_attributes<2>();
+    for (cudaError_t e : {set_attributes<1, false>(), set_attributes<2, false>(), set_attributes<1, true>(),
+                          set_attributes<2, true>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 int vocab_max_pairs()
@@ -958,7 +1034,7 @@ int vocab_max_pairs()
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, vocab_kernel<2>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, vocab_kernel<2, true>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
@@ -970,9 +1046,11 @@ cudaError_t launch_vocab_tiles(const VocabMaps &maps, const VocabTileParams &p, 
 {
     const int n = static_cast<int>(std::min<long long>(static_cast<long long>(p.dh_items) + p.dw_items + p.z_items, workers));
     if (ctas == 2)
-        return launch_kernel_cluster(dependent, 2, vocab_kernel<2>, dim3(2 * n), dim3(THREADS), Shape<2>::SMEM, stream,
+        return launch_kernel_cluster(dependent, 2, p.f16 ? vocab_kernel<2, true> : vocab_kernel<2, false>, dim3(2 * n),
+                                     dim3(THREADS), Shape<2>::SMEM, stream,
                                      maps, p);
-    return launch_kernel(dependent, vocab_kernel<1>, dim3(n), dim3(THREADS), Shape<1>::SMEM, stream, maps, p);
+    return launch_kernel(dependent, p.f16 ? vocab_kernel<1, true> : vocab_kernel<1, false>, dim3(n), dim3(THREADS),
+                         Shape<1>::SMEM, stream, maps, p);
 }
 
 cudaError_t launch_vocab_copy(const void *src, long long ld, int rows, int cols, void *dst, long long ldd, bool dependent,
@@ -982,15 +1060,17 @@ cudaError_t launch_vocab_copy(const void *src, long long ld, int rows, int cols,
                          static_cast<const __nv_bfloat16 *>(src), ld, rows, cols, static_cast<__nv_bfloat16 *>(dst), ldd);
 }
 
-cudaError_t launch_vocab_split(const void *src, long long ld, int rows, int cols, void *f16, float *unscale, void *bf,
-                               int parts, long long ldd, bool dependent, cudaStream_t stream)
+cudaError_t launch_vocab_split(const void *src, long long ld, int rows, int cols, void *f16, float *unscale, int padded,
+                               float *most, float *clear, void *bf, int parts, long long ldd, bool dependent,
+                               cudaStream_t stream)
 {
     const float *s = static_cast<const float *>(src);
     __half *f = static_cast<__half *>(f16);
     __nv_bfloat16 *b = static_cast<__nv_bfloat16 *>(bf);
-    if (bf == nullptr) return launch_split<0>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream);
-    return parts == 2 ? launch_split<2>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream)
-                      : launch_split<3>(s, ld, rows, cols, f, unscale, b, ldd, dependent, stream);
+    if (bf == nullptr)
+        return launch_split<0>(s, ld, rows, cols, f, unscale, padded, most, clear, b, ldd, dependent, stream);
+    return parts == 2 ? launch_split<2>(s, ld, rows, cols, f, unscale, padded, most, clear, b, ldd, dependent, stream)
+                      : launch_split<3>(s, ld, rows, cols, f, unscale, padded, most, clear, b, ldd, dependent, stream);
 }
 
 }  // namespace sgemm_impl

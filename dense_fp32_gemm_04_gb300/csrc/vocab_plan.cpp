@@ -69,7 +69,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.few = !grad && T <= few;
     w.split = f32 && !w.few;
     w.copy_h = f32 ? w.split && q.dw : !w.few && !(q.align_flags & 1);
-    w.copy_w = f32 ? w.split && q.dh : !w.few && !(q.align_flags & 2);
+    w.copy_w = !f32 && !w.few && !(q.align_flags & 2);
     w.ldp = round_up(q.D, 8);
     if (w.copy_h) w.h_off = take(w.parts * T * w.ldp * 2);
     if (w.copy_w) w.w_off = take(w.parts * static_cast<long long>(q.V) * w.ldp * 2);
@@ -77,7 +77,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.hz_off = take(2 * T * w.ldp * 2);
         w.wz_off = take(2 * static_cast<long long>(q.V) * w.ldp * 2);
         w.hs_off = take(T * 4);
-        w.ws_off = take(round_up(q.V, kVocabBN) * 4);
+        w.ws_off = take(256 + round_up(q.V, kVocabBN) * 4);
     }
     if (q.n > 0) {
         w.tid_off = take(T * q.n * 4);
@@ -98,17 +98,19 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.pub.piece = static_cast<int>(std::min<long long>(piece, q.V));
         w.pub.pieces = static_cast<int>((q.V + piece - 1) / piece);
         w.g_blocks = static_cast<int>(piece / 64);
-        w.g_off[0] = take(w.parts * T * piece * 2);
-        w.g_off[1] = w.pub.pieces > 1 ? take(w.parts * T * piece * 2) : w.g_off[0];
+        for (int i = 0; i < std::min(w.pub.pieces, 2); ++i) {
+            w.g_off[i] = q.dw || !w.split ? take(w.parts * T * piece * 2) : 0;
+            w.gz_off[i] = w.split ? q.dh ? take(2 * T * piece * 2) : 0 : w.g_off[i];
+        }
         if (q.dh) {
             // A dH tile's K range is a piece of the vocabulary, the other tiles' are T and D. It is split so far
             // that no part of it takes a worker more than half its share of a launch (the other tiles fill what
             // that leaves uneven), a quarter where there are no others; every split costs a pass over T x D sums.
             const int kblocks = (w.pub.piece + kVocabBK - 1) / kVocabBK;
             const long long tm = (T + bm - 1) / bm, tn = (q.D + kVocabBN - 1) / kVocabBN;
-            const long long own = tm * tn * kblocks;
+            const long long own = tm * tn * kblocks * 3 / (w.products == 6 ? 6 : 3);  // in units of a k-block of dW
             const long long others = q.dw ? (w.pub.piece + bm - 1) / bm * tn * vocab_cost(q.T) : 0;
-            const long long most = std::max<long long>(4, (own + others) / w.workers / (q.dw ? 2 : 4));
+            const long long most = (w.products == 6 ? 2 : 1) * std::max<long long>(4, (own + others) / w.workers / (q.dw ? 2 : 4));
             const long long s = std::max<long long>(1, (kblocks + most - 1) / most);
             w.dh_kb = static_cast<int>((kblocks + s - 1) / s);
             w.dh_splits = (kblocks + w.dh_kb - 1) / w.dh_kb;
