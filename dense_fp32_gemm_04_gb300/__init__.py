@@ -1,8 +1,9 @@
-"""GB300 (sm_103a) single-precision GEMM: C = alpha * A @ B + beta * C, row-major FP32.
+"""GB300 (sm_103a) single-precision GEMM: C = alpha * A @ B + beta * C, row-major FP32,
+and losses over a vocabulary projection with their gradients (FP32 and bfloat16).
 
-Python binding over the library's C ABI (``include/sgemm.h``), by ctypes.
+Python binding over the library's C ABI (``include/sgemm.h``, ``include/sgemm_vocab.h``), by ctypes.
 Everything here is argument marshalling: pointers, leading dimensions and the
-CUDA stream go to ``sgemm_run`` unchanged; every step of the computation runs
+CUDA stream go to the library unchanged; every step of the computation runs
 in the library's CUDA kernels. PyTorch only supplies device memory and
 streams. There is no fallback: if the compiled library is missing, the calls
 raise.
@@ -50,6 +51,7 @@ OPT_FORCE_STREAMK = 8
 OPT_FORCE_TF32_KERNEL = 9
 OPT_FORCE_REPACK_C = 10
 OPT_CLUSTER_SPLIT = 11
+OPT_FORCE_VOCAB_PIECE = 12
 
 
 class Plan(ctypes.Structure):

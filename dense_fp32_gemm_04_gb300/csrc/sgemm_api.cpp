@@ -732,6 +732,10 @@ int sgemm_set_option(sgemm_handle_t h, int option, long long value)
         if (value < -1 || value > 1) return SGEMM_ERR_INVALID_VALUE;
         h->ov.cluster_split = static_cast<int>(value);
         return SGEMM_OK;
+    case SGEMM_OPT_FORCE_VOCAB_PIECE:
+        if (value < 0 || value > (1LL << 30)) return SGEMM_ERR_INVALID_VALUE;
+        h->vocab_piece = static_cast<int>(value);
+        return SGEMM_OK;
     case SGEMM_OPT_FORCE_REPACK_C:
         if (value < -1 || value > 1) return SGEMM_ERR_INVALID_VALUE;
         h->ov.force_repack_c = static_cast<int>(value);

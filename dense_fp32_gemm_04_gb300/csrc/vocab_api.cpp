@@ -46,7 +46,7 @@ VocabProblem problem(const Call &c)
     auto rows16 = [size](const void *p, long long ld) { return aligned(p, 16) && ld * size % 16 == 0; };
     const int align = (rows16(c.H, c.ldh) ? 1 : 0) | (rows16(c.W, c.ldw) ? 2 : 0);
     return VocabProblem{c.T, c.V, c.D, c.dtype, c.n, c.dH != nullptr, c.dW != nullptr, align, c.h->num_sms,
-                        c.h->math_mode, c.h->vocab_pairs};
+                        c.h->math_mode, c.h->vocab_pairs, c.h->vocab_piece};
 }
 
 int check(const Call &c, bool grad)

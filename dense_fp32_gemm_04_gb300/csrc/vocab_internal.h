@@ -1,6 +1,6 @@
 // Interface between the host side of the vocabulary losses (vocab_plan.cpp,
-// vocab_api.cpp) and their kernels (vocab_rows.cu, vocab_kernels.cu). Public
-// contract: include/sgemm_vocab.h. Not installed.
+// vocab_api.cpp) and their kernels (vocab_rows.cu, vocab_few.cu,
+// vocab_kernels.cu). Public contract: include/sgemm_vocab.h. Not installed.
 #pragma once
 
 #include <cstdint>
@@ -39,6 +39,7 @@ struct VocabProblem {
     int num_sms;
     int math_mode;
     int pairs;  // CTA pairs resident at once (0: num_sms / 2; < 0: none)
+    int piece;  // entries per piece of the vocabulary (0: automatic)
 };
 
 // What a call does, and the byte offsets of the parts of its workspace (those a call does not use are empty).

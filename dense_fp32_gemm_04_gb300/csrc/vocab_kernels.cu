@@ -34,8 +34,16 @@
 // pair), 2 and 3 idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4) and
 // columns 128 (w / 8) of the accumulator, so a thread holds 128 columns of one
 // row. That takes more registers than an even share: the first warpgroup hands
-// most of its own over (setmaxnreg). Ring and accumulator barriers are those of the TF32 kernel (tf32_kernels.cu): full /
-// empty per stage, acc_full / acc_empty per accumulator, all waits bounded.
+// most of its own over (setmaxnreg). Ring and accumulator barriers are those of
+// the TF32 kernel (tf32_kernels.cu): full / empty per stage, acc_full / acc_empty
+// per accumulator, all waits bounded.
+//
+// What bounds it: from about 1000 tokens on the tensor cores, which a stage of 32
+// KiB per SM and 512 cycles leaves no slack against the 64 bytes a cycle that an SM
+// can take from the L2 (8192 x 131072 x 4096, one loss: 4.7 ms = 1.87 PFLOP/s
+// for a fresh GPU, 5.3 ms at the clocks of its power limit); below, the operands'
+// way from the L2 and the start of the pipeline in each of a call's launches (256
+// tokens, 32768 x 1024: 25 us for the loss, 65 us for the gradients).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

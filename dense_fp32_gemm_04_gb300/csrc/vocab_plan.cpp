@@ -10,7 +10,8 @@ namespace sgemm_impl {
 namespace {
 
 // dZ of one piece of the vocabulary takes about this much at most (a piece is at least one tile wide), so that
-// two pieces' dZ stay a small part of the logits' size while a launch still has many rounds of tiles.
+// two pieces' dZ stay a small part of the logits' size while a launch still has many rounds of tiles (training 4096
+// tokens, 131072 x 4096: the same time within 2 % from 128 MB to 1 GB).
 constexpr long long kPieceBytes = 256LL << 20;
 
 // Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
@@ -54,10 +55,9 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.products = w.parts * (w.parts + 1) / 2;
     // A pair's 256 rows cost less per row than a CTA's 128, but a last pair that is half empty costs the whole: the
     // loss takes single CTAs where the tokens end in the first half of one of up to three pairs (131072 x 4096, us with
-    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494; 768 tokens
-    // 524 / 508). Of the gradient's products only one has its rows counted in tokens, and its
-    // few tokens leave the pairs' wider tiles waiting for operands: single CTAs up to 256 tokens (711 / 757; 384 tokens
-    // 1015 / 968).
+    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494, 768
+    // tokens 524 / 508). Of the gradient's products only one has its rows counted in tokens, and with few tokens the
+    // wider tiles wait for operands: single CTAs up to 256 tokens (711 / 757; 384 tokens 1015 / 968).
     const int pairs = q.pairs > 0 ? q.pairs : q.pairs < 0 ? 0 : q.num_sms / 2;
     const long long halves = (T + 127) / 128;
     const bool single = grad ? T <= 256 : halves % 2 == 1 && halves <= 5;
@@ -94,7 +94,8 @@ VocabLayout vocab_layout(const VocabProblem &q)
         launches = T > 0 ? launches + 2 : 0;
     } else {
         const long long fit = std::max<long long>(kPieceBytes / (2 * w.parts) / std::max<long long>(T, 1), kVocabBN);
-        const long long piece = std::min<long long>(fit / kVocabBN * kVocabBN, round_up(q.V, kVocabBN));
+        const long long most = q.piece > 0 ? round_up(q.piece, kVocabBN) : fit / kVocabBN * kVocabBN;
+        const long long piece = std::min<long long>(most, round_up(q.V, kVocabBN));
         w.pub.piece = static_cast<int>(std::min<long long>(piece, q.V));
         w.pub.pieces = static_cast<int>((q.V + piece - 1) / piece);
         w.g_blocks = static_cast<int>(piece / 64);
@@ -110,8 +111,9 @@ VocabLayout vocab_layout(const VocabProblem &q)
             const long long tm = (T + bm - 1) / bm, tn = (q.D + kVocabBN - 1) / kVocabBN;
             const long long own = tm * tn * kblocks * 3 / (w.products == 6 ? 6 : 3);  // in units of a k-block of dW
             const long long others = q.dw ? (w.pub.piece + bm - 1) / bm * tn * vocab_cost(q.T) : 0;
-            const long long most = (w.products == 6 ? 2 : 1) * std::max<long long>(4, (own + others) / w.workers / (q.dw ? 2 : 4));
-            const long long s = std::max<long long>(1, (kblocks + most - 1) / most);
+            const long long share = (own + others) / w.workers / (q.dw ? 2 : 4);
+            const long long longest = (w.products == 6 ? 2 : 1) * std::max<long long>(4, share);
+            const long long s = std::max<long long>(1, (kblocks + longest - 1) / longest);
             w.dh_kb = static_cast<int>((kblocks + s - 1) / s);
             w.dh_splits = (kblocks + w.dh_kb - 1) / w.dh_kb;
             w.ldacc = round_up(q.D, 4);
@@ -131,9 +133,16 @@ extern "C" int sgemm_vocab_plan(int T, int V, int D, int dtype, int n, int grad,
 {
     using namespace sgemm_impl;
     if (out == nullptr || (grad != 0 && grad != 1)) return SGEMM_ERR_INVALID_VALUE;
-    const VocabProblem q{T, V, D, dtype, n, grad != 0, grad != 0, align_flags, num_sms, math_mode, 0};
+    VocabProblem q{T, V, D, dtype, n, grad != 0, grad != 0, align_flags, num_sms, math_mode, 0, 0};
     const int rc = validate_vocab(q);
     if (rc != SGEMM_OK) return rc;
     *out = vocab_layout(q).pub;
+    if (grad != 0) {  // a call for one gradient alone splits its work differently: the workspace fits it too
+        for (bool dh : {false, true}) {
+            q.dh = dh;
+            q.dw = !dh;
+            out->workspace_bytes = std::max(out->workspace_bytes, vocab_layout(q).pub.workspace_bytes);
+        }
+    }
     return SGEMM_OK;
 }

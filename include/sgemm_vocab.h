@@ -135,7 +135,8 @@ typedef struct sgemm_vocab_plan_s {
 /*
  * Host-only planning: what the calls above do on a GPU with `num_sms` SMs. n: 0
  * for the cross entropy, else the teacher's entries. grad: 0 for the loss, 1 for
- * the gradients (both of them). align_flags: bit 0 = rows of H are 16-byte
+ * the gradients (both of them; workspace_bytes is enough for either alone too).
+ * align_flags: bit 0 = rows of H are 16-byte
  * aligned (base and row stride), bit 1 = rows of W. Needs no GPU.
  */
 int sgemm_vocab_plan(int T, int V, int D, int dtype, int n, int grad, int align_flags,
