@@ -549,7 +549,7 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
             for (int pr = 6 - product_count(p, w.kind); ok && pr < 6; ++pr) {
                 const int pa = part_a(pr), pb = part_b(pr);
                 for (int kb = s0; kb < s1; ++kb) {
-                    if (!mbar_wait_bounded(smem_addr(&bars->empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
+                    if (!mbar_wait_quiet<false>(smem_addr(&bars->empty[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) {
                         raise_abort(bars, p, kTimeoutCode | kWhereProducerEmpty);
                         ok = false;
                         break;
@@ -594,11 +594,11 @@ __device__ __forceinline__ void produce(const VocabTileParams &p, Bars<Shape<CTA
         const int rec = bars->issued[s];
         if (!(rec & 2)) continue;
         const uint32_t par = static_cast<uint32_t>(rec & 1);
-        if (rank == 0 && !mbar_wait_cluster_bounded(smem_addr(&bars->full[s]), par, nullptr, p.timeout_ns)) {
+        if (rank == 0 && !mbar_wait_quiet<true>(smem_addr(&bars->full[s]), par, nullptr, p.timeout_ns)) {
             report_status(p.status, kTimeoutCode | kWhereDrain);
             break;
         }
-        if (!*abort_flag && !mbar_wait_bounded(smem_addr(&bars->empty[s]), par, abort_flag, p.timeout_ns)) {
+        if (!*abort_flag && !mbar_wait_quiet<false>(smem_addr(&bars->empty[s]), par, abort_flag, p.timeout_ns)) {
             report_status(p.status, kTimeoutCode | kWhereDrain);
             break;
         }
@@ -626,7 +626,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
         for (int s0 = w.kb0; ok && s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
-            if (!mbar_wait_cluster_bounded(smem_addr(&bars->acc_empty[buf]), acc_phase ^ 1u, abort_flag,
+            if (!mbar_wait_quiet<true>(smem_addr(&bars->acc_empty[buf]), acc_phase ^ 1u, abort_flag,
                                            p.timeout_ns)) {
                 raise_abort(bars, p, kTimeoutCode | kWhereAccum);
                 ok = false;
@@ -636,7 +636,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
             const uint32_t d_tmem = tmem + static_cast<uint32_t>(buf * BN);
             const int slabs = (min(s0 + seg, w.kb1) - s0) * product_count(p, w.kind);
             for (int j = 0; j < slabs; ++j) {
-                if (!mbar_wait_cluster_bounded(smem_addr(&bars->full[stage]), phase, abort_flag, p.timeout_ns)) {
+                if (!mbar_wait_quiet<true>(smem_addr(&bars->full[stage]), phase, abort_flag, p.timeout_ns)) {
                     raise_abort(bars, p, kTimeoutCode | kWhereMmaEmpty);
                     ok = false;
                     break;
@@ -677,7 +677,7 @@ __device__ __forceinline__ void issue(const VocabTileParams &p, Bars<Shape<CTAS>
         mma_commit_pair_local(smem_addr(&bars->mma_done));
     else
         mma_commit(smem_addr(&bars->mma_done));
-    if (!mbar_wait_bounded(smem_addr(&bars->mma_done), 0u, nullptr, p.timeout_ns))
+    if (!mbar_wait_quiet<false>(smem_addr(&bars->mma_done), 0u, nullptr, p.timeout_ns))
         report_status(p.status, kTimeoutCode | kWhereDrain);
 }
 
@@ -709,7 +709,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
             const int buf = it & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(it >> 1) & 1u;
-            ok = mbar_wait_cluster_bounded(smem_addr(&bars->acc_full[buf]), acc_phase, abort_flag, p.timeout_ns);
+            ok = mbar_wait_quiet<true>(smem_addr(&bars->acc_full[buf]), acc_phase, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 if (lane == 0) raise_abort(bars, p, kTimeoutCode | kWhereAccum);
