@@ -23,12 +23,15 @@
 // Accumulation: the tensor core truncates its FP32 accumulator at every K = 16
 // step (measured: rel. error 4.4e-6 at K = 4096, all of it toward zero), which a
 // logit of 12 would show in its loss. So a tile's K range is cut into segments
-// (1024 deep for the logits of a loss, 256 deep in every product of FP32
-// operands); the epilogue warps add the segments in registers, rounded to nearest,
-// while the next ones run. A segment's end costs the tensor cores about 600
-// cycles (4096 x 65536 x 4096: 1357 us at 512 deep, 1272 at 1024, 1215 undivided),
-// so what is rounded to bfloat16 in the end (dZ, dW, dH of bfloat16 operands) is
-// one segment: 2^-9 hides what truncation loses.
+// (1024 deep for the logits of a loss, 512 for those of FP32 operands, 256 for
+// their dH and dW); the epilogue warps add the segments in registers, rounded to
+// nearest, while the next ones run. A segment's end costs the tensor cores 600 to
+// 1400 cycles, the time in which the accumulator is read beside them (1024 x 65536
+// x 2048: 190 us at 512 deep, 170 at 1024, 165 undivided), so what is rounded to
+// bfloat16 in the end (dZ, dW, dH of bfloat16 operands) is one segment: 2^-9 hides
+// what truncation loses. Depth and error (2-norm, 2048 x 32768 x 2048 in FP32):
+// 256 throughout dH 4.2e-7, 2.82 ms; 512 for Z 5.3e-7, 2.76 ms; 512 throughout
+// 7.3e-7, 2.76 ms.
 //
 // Warps of a CTA (three warpgroups): 0 TMA producer, 1 MMA issuer (rank 0 of a
 // pair), 2 and 3 idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4) and
@@ -38,11 +41,10 @@
 // the TF32 kernel (tf32_kernels.cu): full / empty per stage, acc_full / acc_empty
 // per accumulator, all waits bounded.
 //
-// What bounds it: from about 1000 tokens on the tensor cores, which a stage of 32
-// KiB per SM and 512 cycles leaves no slack against the 64 bytes a cycle that an SM
-// can take from the L2 (8192 x 131072 x 4096, one loss: 4.7 ms = 1.87 PFLOP/s
-// for a fresh GPU, 5.3 ms at the clocks of its power limit); below, the operands'
-// way from the L2 and the start of the pipeline in each of a call's launches (256
+// What bounds it: from about 1000 tokens on the tensor cores at the clock that the
+// power limit leaves them (8192 x 131072 x 4096, one loss: 4.2 to 4.5 ms = 1.95 to
+// 2.1 PFLOP/s from a cool start, about 5 ms in a loop); below, the operands' way
+// from memory and the start of the pipeline in each of a call's launches (256
 // tokens, 32768 x 1024: 25 us for the loss, 65 us for the gradients).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
