@@ -368,6 +368,18 @@ __device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg,
     }
 }
 
+// dZ of bfloat16 operands is kept divided by the significand of dloss[0], a number in [1, 2), and dH and dW are multiplied
+// by it. The losses' gradients are mostly one number, 1 / tokens, and the label's entry of dZ that number times p - 1:
+// rounded as it is, all labels' entries would be off by much the same share; divided, it lies just below a power of two,
+// where bfloat16 is densest (mean loss of an untrained head, dH off by 1.68e-3 of its norm, which is the result's own
+// rounding; undivided 1.70e-3 over 1000 tokens, 1.99e-3 over 700, 2.43e-3 over 513).
+__device__ __forceinline__ float significand(const VocabTileParams &p)
+{
+    if (p.dloss == nullptr) return 1.0f;
+    const uint32_t bits = __float_as_uint(p.dloss[0]), exponent = bits >> 23 & 255u;
+    return exponent == 0 || exponent == 255 ? 1.0f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+}
+
 // What a thread needs to know of its row before the tile is there: fetched while the products run.
 struct Row {
     int entry, id;   // the first target with an id of at least the tile's first column, and that id
@@ -387,7 +399,7 @@ __device__ __forceinline__ void load_target(const VocabTileParams &p, Row &r, lo
 }
 
 template <bool F16>
-__device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row, int c0, bool dz)
+__device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row, int c0, bool dz, float divide)
 {
     Row r{};
     r.id = kNoTarget;
@@ -413,7 +425,7 @@ __device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row,
         load_target(p, r, row);
     }
     if (dz) {
-        if (r.used) r.g = p.dloss[row];
+        if (r.used) r.g = F16 ? p.dloss[row] : p.dloss[row] / divide;
         r.lse = p.lse[row];
     }
     return r;
@@ -695,6 +707,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
     const int quarter = warp & 3, half = warp >> 3;
     unsigned char *area = staging + (warp - 4) * kWarpStaging;
     const uint32_t stg = smem_addr(area);
+    const float divide = F16 ? 1.0f : significand(p);
     int it = 0;
     bool ok = true;
     Item w;
@@ -705,7 +718,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         const int c0 = w.n0 + half * COLS;
         Row r{};
         if (w.kind == kVocabLoss || w.kind == kVocabDz)
-            r = load_row<F16>(p, r0 + lane, p.z_v0 + c0, w.kind == kVocabDz);
+            r = load_row<F16>(p, r0 + lane, p.z_v0 + c0, w.kind == kVocabDz, divide);
         else if (F16 && w.kind == kVocabDh)
             r.g = load_dloss(p, r0 + lane);
         for (int s0 = w.kb0; s0 < w.kb1; s0 += seg, ++it) {
@@ -757,7 +770,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
         const CUtensorMap *map = &maps.dW;
         const bool wide = w.kind == kVocabDh || (w.kind == kVocabDw && p.dtype == SGEMM_DTYPE_F32);
         int row = r0, cols = p.D, parts = 1, blocks = 0;
-        float alpha = p.alpha;
+        float alpha = F16 ? p.alpha : p.alpha * divide;
         bool inside = r0 < p.T;
         if (w.kind == kVocabDz) {
             make_dz<F16>(p, acc, r, r0 + lane, p.z_v0 + c0);
@@ -787,10 +800,10 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             const long long at = static_cast<long long>(row) * p.lddw + c0;
             if (wide)
                 write_rows(acc, reinterpret_cast<float *>(area), lane, static_cast<float *>(p.dW) + at, p.lddw,
-                           p.g_vn - r0, p.D - c0, p.dw_vec, p.alpha, p.beta);
+                           p.g_vn - r0, p.D - c0, p.dw_vec, alpha, p.beta);
             else
                 write_rows(acc, reinterpret_cast<float *>(area), lane, static_cast<__nv_bfloat16 *>(p.dW) + at, p.lddw,
-                           p.g_vn - r0, p.D - c0, p.dw_vec, p.alpha, p.beta);
+                           p.g_vn - r0, p.D - c0, p.dw_vec, alpha, p.beta);
         } else if (wide) {
             send_f32(map, acc, stg, lane, c0, row, w.split, cols, w.kind == kVocabDh && p.acc_add, alpha);
         } else {

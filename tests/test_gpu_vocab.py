@@ -346,6 +346,26 @@ def test_captured_into_a_graph():
     handle.close()
 
 
+@pytest.mark.parametrize("tokens", [1000, 700, 1023, 513])
+def test_the_mean_loss_does_not_round_all_labels_alike(h, tokens):
+    """dloss = 1 / tokens for all: the label's entry of dZ is that number times p - 1, p small for an untrained head.
+
+    Where dZ is held next to a power of two from below, its rounding to 8 bits is at most 2^-7 / sqrt(12) / 1.98 = 1.1e-3
+    of it (2-norm), the result's 2^-7 / sqrt(24) = 1.6e-3 for significands spread over [1, 2): 2.0e-3 together. Held
+    anywhere it could be off by 2^-8 for all tokens alike."""
+    V, D = 5000, 256
+    H, W, gen = _operands(tokens, V, D, BF16, spread=0.5)
+    labels = _labels(gen, tokens, V, 0.0)
+    dloss = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    got = _xent(h, H, W, labels, dloss)
+    _status(h)
+    ref = vr.reference(H, W, 1.0, 1.0, *vr.xent_targets(labels, V), dloss, bf16=True)
+    for name in ("dH", "dW"):
+        vr.check(name, got[name], ref[name])
+        value = ref[name][0]
+        assert (got[name].cpu().double() - value).norm() < 2.3e-3 * value.norm(), name
+
+
 @pytest.mark.parametrize("op", ["xent", "distill"])
 def test_gradients_against_differences(h, op):
     """Directional derivatives of the summed loss by central differences of the library's own losses, FP32.
