@@ -15,9 +15,9 @@ namespace {
 constexpr long long kPieceBytes = 256LL << 20;
 
 // Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
-// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 82 / 279, 24
-// tokens 230 / 278, 32 tokens 301 / 278; bfloat16 131072 x 4096, 2 tokens 158 / 178, 3 tokens 233 / 177; rows at an odd
-// stride, 50021 x 1531, 8 tokens 86 / 92.
+// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 82 / 281, 24
+// tokens 230 / 281, 32 tokens 302 / 281; bfloat16 131072 x 4096, 2 tokens 164 / 172, 3 tokens 290 / 173; rows at an odd
+// stride, 50021 x 1531, 8 tokens 87 / 92, 12 tokens 165 / 92.
 constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
@@ -55,12 +55,14 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.products = w.parts * (w.parts + 1) / 2;
     // A pair's 256 rows cost less per row than a CTA's 128, but a last pair that is half empty costs the whole: the
     // loss takes single CTAs where the tokens end in the first half of one of up to three pairs (131072 x 4096, us with
-    // single CTAs / pairs: 128 tokens 176 / 183, 256 tokens 205 / 191, 384 tokens 289 / 324, 640 tokens 453 / 494, 768
-    // tokens 524 / 508). Of the gradient's products only one has its rows counted in tokens, and with few tokens the
-    // wider tiles wait for operands: single CTAs up to 256 tokens (711 / 757; 384 tokens 1015 / 968).
+    // single CTAs / pairs: 128 tokens 173 / 178, 256 tokens 202 / 184, 384 tokens 281 / 300, 640 tokens 448 / 450, 768
+    // tokens 525 / 460). Of the gradient's products only one has its rows counted in tokens, and with few tokens the
+    // wider tiles wait for operands: single CTAs up to 384 tokens (128 tokens 626 / 687, 256 tokens 699 / 741, 300
+    // tokens 867 / 894, 384 tokens 974 / 933, but 203 / 206 at 50021 x 2048 and 86 / 88 at 32768 x 1024; 500 tokens
+    // 1187 / 981).
     const int pairs = q.pairs > 0 ? q.pairs : q.pairs < 0 ? 0 : q.num_sms / 2;
     const long long halves = (T + 127) / 128;
-    const bool single = grad ? T <= 256 : halves % 2 == 1 && halves <= 5;
+    const bool single = grad ? halves <= 3 : halves % 2 == 1 && halves <= 5;
     w.ctas = single || pairs == 0 ? 1 : 2;
     w.workers = w.ctas == 2 ? pairs : q.num_sms;
     const int bm = 128 * w.ctas;
