@@ -54,8 +54,9 @@
  * dW are rounded once. FP32 operands enter the tensor cores as sums of 16-bit
  * parts: for the logits two float16 parts (22 bits) of rows scaled by powers of
  * two, for dH and dW, with dZ split likewise, three bfloat16 parts (24 bits; two
- * parts with SGEMM_MATH_TF32). Results are bitwise reproducible for a fixed shape,
- * alignment and plan.
+ * parts with SGEMM_MATH_TF32). Probabilities and entries of dZ below FP32's normal
+ * range (2^-126) may count as 0. Results are bitwise reproducible for a fixed
+ * shape, alignment and plan.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.
  * T, V or D so large that their tiles do not count in 32 bits: SGEMM_ERR_NOT_SUPPORTED.
