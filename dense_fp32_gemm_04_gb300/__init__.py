@@ -154,7 +154,7 @@ def plan(M, N, K, lda=None, ldb=None, ldc=None, align_flags=7, num_sms=152, math
     return p
 
 
-def vocab_plan(T, V, D, dtype=DTYPE_BF16, n=0, grad=False, align_flags=3, num_sms=152,
+def vocab_plan(T, V, D, dtype=DTYPE_BF16, n=0, grad=False, align_flags=15, num_sms=152,
                math_mode=MATH_FP32) -> VocabPlan:
     """Host-only: what a vocabulary loss (``n`` teacher entries, 0 for the cross entropy) or its gradients would do."""
     p = VocabPlan()

@@ -43,8 +43,9 @@ bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t
 VocabProblem problem(const Call &c)
 {
     const int size = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
-    auto rows16 = [size](const void *p, long long ld) { return aligned(p, 16) && ld * size % 16 == 0; };
-    const int align = (rows16(c.H, c.ldh) ? 1 : 0) | (rows16(c.W, c.ldw) ? 2 : 0);
+    auto rows = [size](const void *p, long long ld, unsigned bytes) { return aligned(p, bytes) && ld * size % bytes == 0; };
+    const int align = (rows(c.H, c.ldh, 16) ? 1 : 0) | (rows(c.W, c.ldw, 16) ? 2 : 0) | (rows(c.H, c.ldh, 128) ? 4 : 0) |
+                      (rows(c.W, c.ldw, 128) ? 8 : 0);
     return VocabProblem{c.T, c.V, c.D, c.dtype, c.n, c.dH != nullptr, c.dW != nullptr, align, c.h->num_sms,
                         c.h->math_mode, c.h->vocab_pairs, c.h->vocab_piece};
 }
@@ -200,7 +201,7 @@ int run_loss(const Call &c)
     if (w.few) {
         const VocabFewParams f{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0,
                                c.h->d_status};
-        const bool vec = problem(c).align_flags == 3;
+        const bool vec = (problem(c).align_flags & 3) == 3;
         if (launch_vocab_few(f, c.dtype, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
         return SGEMM_ERR_LAUNCH;

@@ -1,5 +1,5 @@
 // Losses of a few tokens (scoring calls). The head's bytes are the cost. For FP32
-// the tensor-core path would first write W as bfloat16 parts and read those, 4
+// the tensor-core path would first write W as 16-bit parts and read those, 3.5
 // times its size in all; for bfloat16 its tiles of 128 tokens x 256 entries leave
 // SMs idle or uneven in a single wave. Here every row of W is read once, as it
 // is, by warps with equal shares of the vocabulary.

@@ -35,7 +35,7 @@ struct VocabProblem {
     int dtype;  // sgemm_dtype_t
     int n;      // teacher entries per token, 0 = cross entropy
     bool dh, dw;  // gradients asked for (both false: the loss)
-    int align_flags;
+    int align_flags;  // as sgemm_vocab_plan's
     int num_sms;
     int math_mode;
     int pairs;  // CTA pairs resident at once (0: num_sms / 2; < 0: none)

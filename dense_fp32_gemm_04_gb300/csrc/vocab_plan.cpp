@@ -20,6 +20,12 @@ constexpr long long kPieceBytes = 256LL << 20;
 // stride, 50021 x 1531, 8 tokens 87 / 92, 12 tokens 165 / 92.
 constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
 
+// From this many tokens on bfloat16 rows that do not start on 128-byte lines are copied to rows that do, though the copy
+// engine could read them: a slab's row is then one line and not parts of two (50000 x 1496, loss in us, read as they are
+// / with the copies: 2048 tokens 242 / 232, 4096 tokens 446 / 399; gradients 589 / 590 and 1155 / 1110; with rows on
+// lines from the start 337 and 1030 at 4096 tokens).
+constexpr int kLineTokens = 2048;
+
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 }  // namespace
@@ -28,7 +34,7 @@ int validate_vocab(const VocabProblem &q)
 {
     if (q.T < 0 || q.V < 1 || q.D < 1 || q.n < 0) return SGEMM_ERR_INVALID_VALUE;
     if (q.dtype != SGEMM_DTYPE_F32 && q.dtype != SGEMM_DTYPE_BF16) return SGEMM_ERR_INVALID_VALUE;
-    if (q.align_flags < 0 || q.align_flags > 3 || q.num_sms < 1) return SGEMM_ERR_INVALID_VALUE;
+    if (q.align_flags < 0 || q.align_flags > 15 || q.num_sms < 1) return SGEMM_ERR_INVALID_VALUE;
     if (q.math_mode != SGEMM_MATH_FP32 && q.math_mode != SGEMM_MATH_TF32) return SGEMM_ERR_INVALID_VALUE;
     if (q.n > SGEMM_DISTILL_MAX_ENTRIES) return SGEMM_ERR_NOT_SUPPORTED;
     // tiles and coordinates are counted in 32 bits
@@ -67,12 +73,13 @@ VocabLayout vocab_layout(const VocabProblem &q)
     w.workers = w.ctas == 2 ? pairs : q.num_sms;
     const int bm = 128 * w.ctas;
 
-    const int few = f32 ? kFewTokensF32 : q.align_flags == 3 ? kFewTokensBf16 : kFewTokensCopied;
+    const int few = f32 ? kFewTokensF32 : (q.align_flags & 3) == 3 ? kFewTokensBf16 : kFewTokensCopied;
     w.few = !grad && T <= few;
     w.split = f32 && !w.few;
-    w.copy_h = f32 ? w.split && q.dw : !w.few && !(q.align_flags & 1);
-    w.copy_w = !f32 && !w.few && !(q.align_flags & 2);
-    w.ldp = round_up(q.D, 8);
+    const int lines = T >= kLineTokens ? 5 : 1;  // the flags that spare H's copy; W's are the next bits
+    w.copy_h = f32 ? w.split && q.dw : !w.few && (q.align_flags & lines) != lines;
+    w.copy_w = !f32 && !w.few && (q.align_flags >> 1 & lines) != lines;
+    w.ldp = round_up(q.D, 64);  // whole 128-byte lines: a copied row of a slab is one of them, not parts of two
     if (w.copy_h) w.h_off = take(w.parts * T * w.ldp * 2);
     if (w.copy_w) w.w_off = take(w.parts * static_cast<long long>(q.V) * w.ldp * 2);
     if (w.split) {

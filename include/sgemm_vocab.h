@@ -44,9 +44,9 @@
  *   - dH or dW may be NULL: that gradient is not computed. They must not overlap
  *     H or W.
  *   - T == 0: the losses do nothing; the gradients give dW = beta * dW.
- *   - Rows of H, W, dH and dW need no alignment beyond their element's; 16-byte
- *     aligned operands and row strides spare a copy of bfloat16 operands into the
- *     workspace.
+ *   - Rows of H, W, dH and dW need no alignment beyond their element's; rows of H
+ *     and W on 16-byte boundaries (on 128-byte ones from 2048 tokens on) spare a
+ *     copy of bfloat16 operands into the workspace.
  *
  * Numerics: loss and lse are FP32 whatever the operands' type; products are
  * accumulated in FP32, softmax statistics are kept in FP32. bfloat16 operands
@@ -137,8 +137,8 @@ typedef struct sgemm_vocab_plan_s {
  * Host-only planning: what the calls above do on a GPU with `num_sms` SMs. n: 0
  * for the cross entropy, else the teacher's entries. grad: 0 for the loss, 1 for
  * the gradients (both of them; workspace_bytes is enough for either alone too).
- * align_flags: bit 0 = rows of H are 16-byte
- * aligned (base and row stride), bit 1 = rows of W. Needs no GPU.
+ * align_flags: bit 0 = rows of H are 16-byte aligned (base and row stride), bit 1 =
+ * rows of W, bits 2 and 3 = the same with 128 bytes. Needs no GPU.
  */
 int sgemm_vocab_plan(int T, int V, int D, int dtype, int n, int grad, int align_flags,
                      int num_sms, int math_mode, sgemm_vocab_plan_t *out);

@@ -53,6 +53,19 @@ def test_plan_covers_the_vocabulary(lib, dtype, grad):
     assert p.pieces > 1
 
 
+def test_plan_copies_rows_off_their_lines(lib):
+    """bfloat16 rows that are not 16-byte aligned are copied, from 2048 tokens on those off 128-byte lines too."""
+    V, D = 50000, 1496
+
+    def launches(T, align):
+        return sg.vocab_plan(T, V, D, align_flags=align).launches
+
+    for T in (500, 2047):
+        assert launches(T, 0) == launches(T, 3) + 2 == launches(T, 15) + 2 == launches(T, 1) + 1
+    for T in (2048, 9000):
+        assert launches(T, 0) == launches(T, 3) == launches(T, 15) + 2 == launches(T, 7) + 1
+
+
 def test_plan_refusals(lib):
     p = sg.VocabPlan()
 
@@ -61,7 +74,7 @@ def test_plan_refusals(lib):
 
     assert plan() == sg.SGEMM_OK
     for bad in (dict(T=-1), dict(V=0), dict(D=0), dict(dtype=2), dict(dtype=-1), dict(n=-1), dict(grad=2),
-                dict(align=4), dict(sms=0), dict(mode=5), dict(out=None)):
+                dict(align=16), dict(align=-1), dict(sms=0), dict(mode=5), dict(out=None)):
         assert plan(**bad) == sg.SGEMM_ERR_INVALID_VALUE, bad
     assert plan(n=1025) == sg.SGEMM_ERR_NOT_SUPPORTED
 
