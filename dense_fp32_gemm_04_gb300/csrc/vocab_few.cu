@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             const float base = top == -kInf ? 0.0f : top;
             s *= exp2f(m - base);
 #pragma unroll
-            for (int r = 0; r < R; ++r) s += exp2f(fmaf(z[r], k, -base));
+            for (int r = 0; r < R; ++r)  // (M so large that its rounding would show: the products rounded as it was)
+                s += exp2f(fabsf(base) < kHugeLog2 ? fmaf(z[r], k, -base) : __fmul_rn(k, z[r]) - base);
             m = top;
             if (p.t.labels != nullptr) {
                 const long long y = p.t.labels[token];

@@ -19,6 +19,9 @@ namespace sgemm_impl {
 // that are left out at the end with the id kNoTarget.
 constexpr int kNoTarget = 0x7fffffff;
 
+// Logits in powers of two whose FP32 neighbours are 2 and more apart.
+constexpr float kHugeLog2 = 16777216.0f;
+
 struct VocabTargets {
     const long long *labels;  // cross entropy, else NULL
     int n;                    // targets per token (1 for the cross entropy)

@@ -368,6 +368,15 @@ __device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg,
     }
 }
 
+// dloss of a token, 0 for a masked one.
+__device__ __forceinline__ float load_dloss(const VocabTileParams &p, long long row)
+{
+    if (row >= p.T) return 0.0f;
+    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
+    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
+    return used ? p.dloss[row] : 0.0f;
+}
+
 // dZ of bfloat16 operands is kept divided by the significand of dloss[0], a number in [1, 2), and dH and dW are multiplied
 // by it. The losses' gradients are mostly one number, 1 / tokens, and the label's entry of dZ that number times p - 1:
 // rounded as it is, all labels' entries would be off by much the same share; divided, it lies just below a power of two,
@@ -376,7 +385,7 @@ __device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg,
 __device__ __forceinline__ float significand(const VocabTileParams &p)
 {
     if (p.dloss == nullptr) return 1.0f;
-    const uint32_t bits = __float_as_uint(p.dloss[0]), exponent = bits >> 23 & 255u;
+    const uint32_t bits = __float_as_uint(load_dloss(p, 0)), exponent = bits >> 23 & 255u;  // a masked token's may be anything
     return exponent == 0 || exponent == 255 ? 1.0f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
 }
 
@@ -431,15 +440,6 @@ __device__ __forceinline__ Row load_row(const VocabTileParams &p, long long row,
     return r;
 }
 
-// dloss of a token, 0 for a masked one.
-__device__ __forceinline__ float load_dloss(const VocabTileParams &p, long long row)
-{
-    if (row >= p.T) return 0.0f;
-    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
-    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
-    return used ? p.dloss[row] : 0.0f;
-}
-
 // f(column - c0) for the row's targets in [c0, c0 + 128) one after the other; r.entry and r.q are the target's.
 template <typename F>
 __device__ __forceinline__ void for_targets(const VocabTileParams &p, Row &r, long long row, int c0, F f)
@@ -473,7 +473,8 @@ __device__ __forceinline__ void unscale_columns(const float *__restrict__ factor
 
 // Z tile of a loss call: the softmax statistics of the thread's columns, and the logits at its targets. z = scale * acc;
 // the exponentials are powers of two, exp(z - m) = 2^(k acc - M) with k = scale log2(e) and M = k max(acc) rounded: M is
-// what the pair holds, so its rounding costs nothing.
+// what the pair holds, so its rounding costs nothing, until M's last bit is worth as much as the range of an exponential:
+// from kHugeLog2 on the other products are rounded as M was, none of which is then above it.
 __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
     const int cols = p.V - c0;  // columns of the vocabulary from c0 on
@@ -484,8 +485,21 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     float m[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
     for (int i = 0; i < COLS; ++i) m[i & 3] = fmaxf(m[i & 3], z[i]);
-    const float k = r.scale * kLog2e, top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for_targets(p, r, row, c0, [&](int at) {
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
+        if (index_ok(row < p.T && r.entry >= 0 && r.entry < p.t.n, p.status, kWhereIdxVocabTarget))
+            p.zt[row * p.t.n + r.entry] = r.scale * x;
+    });
+    float k = r.scale * kLog2e;
+    const float top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     const float base = top == -kInf ? 0.0f : -top;
+    if (fabsf(base) >= kHugeLog2) {  // products rounded as M was
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) z[i] = __fmul_rn(k, z[i]);
+        k = 1.0f;
+    }
     const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(base, base);
     unsigned long long s2[4] = {};
 #pragma unroll
@@ -498,13 +512,6 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
     unpack_f32x2(add_f32x2(add_f32x2(s2[0], s2[1]), add_f32x2(s2[2], s2[3])), x, y);
     if (row < p.T && index_ok(c0 / COLS < p.stat_cols, p.status, kWhereIdxVocabStat))
         p.part[static_cast<long long>(c0 / COLS) * p.T + row] = make_float2(top, x + y);
-    for_targets(p, r, row, c0, [&](int at) {
-        float x = 0.0f;
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) x = i == at ? z[i] : x;
-        if (index_ok(row < p.T && r.entry >= 0 && r.entry < p.t.n, p.status, kWhereIdxVocabTarget))
-            p.zt[row * p.t.n + r.entry] = r.scale * x;
-    });
 }
 
 // Z tile of a gradient call, made into dZ / alpha = dloss (exp(z - lse) - q); for float16
@@ -513,14 +520,19 @@ template <bool F16>
 __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COLS], Row &r, long long row, int c0)
 {
     // exp(z - lse) = 2^(k acc - L) 2^-l with L + l = lse log2(e), L rounded and l its remainder: l goes into the factor.
+    // No probability is above 1: with a huge lse (1e9 is a multiple of 64) p, or l's factor, could leave the range of
+    // FP32 or of dZ's parts. (A NaN logit has made lse NaN, and so l, which passes.)
     const float k = r.scale * kLog2e, L = r.lse * kLog2e;
-    const float l = fmaf(r.lse, kLog2e, -L) + r.lse * kLog2eLow;
+    float l = fmaf(r.lse, kLog2e, -L) + r.lse * kLog2eLow;
+    l = l > 100.0f ? 100.0f : l < -100.0f ? -100.0f : l;
     const float weight = F16 ? 1.0f : r.g, g = weight * exp2_approx(-l);
     const unsigned long long k2 = pack_f32x2(k, k), b2 = pack_f32x2(-L, -L), g2 = pack_f32x2(g, g);
 #pragma unroll
     for (int i = 0; i < COLS; i += 2) {
         float x, y;
         unpack_f32x2(fma_f32x2(pack_f32x2(z[i], z[i + 1]), k2, b2), x, y);
+        x = fminf(x, l);
+        y = fminf(y, l);
         unpack_f32x2(mul_f32x2(pack_f32x2(exp2_approx(x), exp2_approx(y)), g2), z[i], z[i + 1]);
     }
     // a masked token's dZ is 0 whatever its logits are; so is dZ past the vocabulary, which the products do read
@@ -905,7 +917,7 @@ vocab_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ Voc
     }
 }
 
-// bfloat16 rows at any stride -> rows at a 16-byte stride. 64 threads per row, two elements each: 4-byte stores, and loads
+// bfloat16 rows at any stride -> rows on 128-byte lines. 64 threads per row, two elements each: 4-byte stores, and loads
 // that need no alignment (50021 x 1531: 49 us, 6.3 TB/s).
 __global__ void __launch_bounds__(256)
 vocab_copy_kernel(const __nv_bfloat16 *__restrict__ src, long long ld, int rows, int cols,
@@ -924,7 +936,7 @@ vocab_copy_kernel(const __nv_bfloat16 *__restrict__ src, long long ld, int rows,
     }
 }
 
-// FP32 rows at any stride -> 16-bit parts at a 16-byte row stride, a warp per row:
+// FP32 rows at any stride -> 16-bit parts in rows on 128-byte lines, a warp per row:
 //   f16:  x 2^s = x0 + x1 in float16, s for each row such that its largest finite element lands in [2^14, 2^15);
 //         2^-s is kept (2^-126 for rows without such an element and for those up to `padded`), and the largest of
 //         them in *most; *clear is the next such word to set to 0. (The row is read a second time from the cache.)

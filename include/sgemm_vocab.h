@@ -52,11 +52,15 @@
  * accumulated in FP32, softmax statistics are kept in FP32. bfloat16 operands
  * enter the products as they are and dZ enters them rounded to bfloat16; dH and
  * dW are rounded once. FP32 operands enter the tensor cores as sums of 16-bit
- * parts: for the logits two float16 parts (22 bits) of rows scaled by powers of
- * two, for dH and dW, with dZ split likewise, three bfloat16 parts (24 bits; two
- * parts with SGEMM_MATH_TF32). Probabilities and entries of dZ below FP32's normal
- * range (2^-126) may count as 0. Results are bitwise reproducible for a fixed
- * shape, alignment and plan.
+ * parts: for the logits and dH two float16 parts (22 bits) of rows scaled by
+ * powers of two, for dW three bfloat16 parts (24 bits; two parts with
+ * SGEMM_MATH_TF32). For dH, entry v of dZ is held to within 2^-39 dloss (max |W|
+ * of all rows) / (max |W| of row v): a row of W a million times larger than the
+ * others leaves 3e-4 of dH where the others make it up. The gradients' p comes
+ * from lse as it is stored, an FP32 number: its relative error grows as
+ * 2^-22 |lse|, and p is held to at most 1. Probabilities and entries of dZ below
+ * FP32's normal range (2^-126) may count as 0. Results are bitwise reproducible
+ * for a fixed shape, alignment and plan.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.
  * T, V or D so large that their tiles do not count in 32 bits: SGEMM_ERR_NOT_SUPPORTED.
