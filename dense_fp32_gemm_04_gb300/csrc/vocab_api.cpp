@@ -150,11 +150,12 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     p->parts = w.parts;
     p->products = w.products;
     p->f16_products = w.split ? 3 : 1;
-    // Segments (vocab_kernels.cu): 1024 deep for the logits of a loss, 512 for those of FP32 operands (the same in the
-    // loss and the gradients: what truncation takes cancels in exp(z - lse)), 256 for their dH and dW, whole for what is
-    // rounded to bfloat16.
+    // Segments (vocab_kernels.cu): 1024 deep for logits, 512 for those of FP32 operands, in the loss and in the gradients
+    // alike: what truncation takes of a logit is then in lse too and cancels in exp(z - lse), which the label's entry of
+    // dZ, p - 1, needs however dZ is rounded afterwards. 256 for dH and dW of FP32 operands, whole where they are rounded
+    // to bfloat16.
     const int whole = 1 << 24;
-    p->seg_z = w.split ? 8 : c.dH == nullptr && c.dW == nullptr ? 16 : whole;
+    p->seg_z = w.split ? 8 : 16;
     p->seg_g = w.split ? 4 : whole;
     p->scale = c.scale;
     p->lse = c.lse;

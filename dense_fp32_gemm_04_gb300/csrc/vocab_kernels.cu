@@ -21,17 +21,21 @@
 // parts (24 bits at any magnitude), 6 products.
 //
 // Accumulation: the tensor core truncates its FP32 accumulator at every K = 16
-// step (measured: rel. error 4.4e-6 at K = 4096, all of it toward zero), which a
-// logit of 12 would show in its loss. So a tile's K range is cut into segments
-// (1024 deep for the logits of a loss, 512 for those of FP32 operands, 256 for
-// their dH and dW); the epilogue warps add the segments in registers, rounded to
-// nearest, while the next ones run. A segment's end costs the tensor cores 600 to
-// 1400 cycles, the time in which the accumulator is read beside them (1024 x 65536
-// x 2048: 190 us at 512 deep, 170 at 1024, 165 undivided), so what is rounded to
-// bfloat16 in the end (dZ, dW, dH of bfloat16 operands) is one segment: 2^-9 hides
-// what truncation loses. Depth and error (2-norm, 2048 x 32768 x 2048 in FP32):
-// 256 throughout dH 4.2e-7, 2.82 ms; 512 for Z 5.3e-7, 2.76 ms; 512 throughout
-// 7.3e-7, 2.76 ms.
+// step (measured: rel. error 4.4e-6 at K = 4096 and up to 1.3e-5 where one sign
+// prevails, all of it toward zero), which a logit of 12 would show in its loss. So
+// a tile's K range is cut into segments (1024 deep for logits, 512 for those of
+// FP32 operands, 256 for their dH and dW); the epilogue warps add the segments in
+// registers, rounded to nearest, while the next ones run. A segment's end costs the
+// tensor cores 600 to 1400 cycles, the time in which the accumulator is read beside
+// them (1024 x 65536 x 2048: 190 us at 512 deep, 170 at 1024, 165 undivided).
+// Logits are cut alike in a loss and in its gradients: the two calls then truncate
+// them to the same bits, and p = exp(z - lse) does not see it. (Undivided in the
+// gradients, p of a label's logit of 64 at K = 4096 was 8e-4 low, as much as the
+// label's whole entry p - 1 where the token is learnt.) What is rounded to bfloat16
+// in the end and subtracted from nothing (dW, dH of bfloat16 operands) is one
+// segment: 2^-9 hides what truncation loses. Depth and error (2-norm, 2048 x 32768
+// x 2048 in FP32): 256 throughout dH 4.2e-7, 2.82 ms; 512 for Z 5.3e-7, 2.76 ms;
+// 512 throughout 7.3e-7, 2.76 ms.
 //
 // Warps of a CTA (three warpgroups): 0 TMA producer, 1 MMA issuer (rank 0 of a
 // pair), 2 and 3 idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4) and
