@@ -152,10 +152,12 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     p->f16_products = w.split ? 3 : 1;
     // Segments (vocab_kernels.cu): 1024 deep for logits, 512 for those of FP32 operands, in the loss and in the gradients
     // alike: what truncation takes of a logit is then in lse too and cancels in exp(z - lse), which the label's entry of
-    // dZ, p - 1, needs however dZ is rounded afterwards. 256 for dH and dW of FP32 operands, whole where they are rounded
-    // to bfloat16.
+    // dZ, p - 1, needs however dZ is rounded afterwards. The loss of a few tokens truncates nothing: their gradients
+    // take the label's logit from its kernel (vocab_few.cu) and cut the others, in FP32, 64 deep (24 x 50021 x 4096: 1052
+    // us at 512, 1054 at 128, 1063 at 64; a probability at a logit of 50 off by 1.2e-4, 3e-5 and 1.5e-5 of itself). 256
+    // for dH and dW of FP32 operands, whole where they are rounded to bfloat16.
     const int whole = 1 << 24;
-    p->seg_z = w.split ? 8 : 16;
+    p->seg_z = w.split ? w.few_targets ? 1 : 8 : 16;
     p->seg_g = w.split ? 4 : whole;
     p->scale = c.scale;
     p->lse = c.lse;
@@ -176,6 +178,13 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     }
     return SGEMM_OK;
 }
+
+VocabFewParams few_params(const Call &c, const VocabTileParams &p)
+{
+    return VocabFewParams{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0, c.h->d_status};
+}
+
+bool few_vec(const Call &c) { return (problem(c).align_flags & 3) == 3; }
 
 int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
@@ -200,10 +209,8 @@ int run_loss(const Call &c)
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
     p.stat_cols = w.stat_cols;
     if (w.few) {
-        const VocabFewParams f{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0,
-                               c.h->d_status};
-        const bool vec = (problem(c).align_flags & 3) == 3;
-        if (launch_vocab_few(f, c.dtype, vec, c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        const VocabFewParams f = few_params(c, p);
+        if (launch_vocab_few(f, c.dtype, few_vec(c), c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
         return SGEMM_ERR_LAUNCH;
     }
@@ -231,6 +238,11 @@ int run_grad(const Call &c)
     VocabTileParams p{};
     VocabMaps m;
     if ((rc = begin(c, w, &p, &m)) != SGEMM_OK) return rc;
+    if (w.few_targets) {
+        p.zt = reinterpret_cast<float *>(ws + w.zt_off);
+        if (launch_vocab_few_targets(few_params(c, p), c.dtype, few_vec(c), c.dependent(), c.stream) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+    }
     const int bm = 128 * w.ctas, tm = ceil_div(c.T, bm), tn = ceil_div(c.D, kVocabBN);
     const int elem = c.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     p.z_kind = kVocabDz;

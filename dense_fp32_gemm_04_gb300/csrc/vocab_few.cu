@@ -188,6 +188,38 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
     }
 }
 
+// The products at the targets alone, a warp for each, for the gradients of tokens whose loss came from the kernel above:
+// the same sums in the same order (reduce_scatter adds what a butterfly adds), so the label's entry p - 1 of dZ is made of
+// the very logit in lse, where the tensor cores' truncated one would be off by up to 2^-18 of itself (1 token, 32768 x 2048:
+// 5 us of the call's 90).
+template <typename E, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32) vocab_few_targets_kernel(const VocabFewParams p)
+{
+    constexpr int PART = kPerLane<E, VEC>, STEP = 32 * PART;
+    const int lane = threadIdx.x & 31, pair = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (pair >= p.T * p.t.n) return;
+    const int token = pair / p.t.n;
+    const long long y = p.t.labels != nullptr ? p.t.labels[token] : p.t.id[pair];
+    if (y < 0 || y >= p.V) return;  // (kNoTarget too)
+    const E *h = static_cast<const E *>(p.H) + token * p.ldh, *w = static_cast<const E *>(p.W) + y * p.ldw;
+    const int whole = p.D / STEP * STEP;
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int d = 0; d < whole; d += STEP) {
+        float a[PART], b[PART];
+        load_part<E, VEC, false>(w, d, lane, a);
+        load_part<E, VEC, false>(h, d, lane, b);
+#pragma unroll
+        for (int i = 0; i < PART; ++i) acc = fmaf(a[i], b[i], acc);
+    }
+    for (int d = whole + lane; d < p.D; d += 32)
+        acc = fmaf(static_cast<float>(__ldg(w + d)), static_cast<float>(__ldg(h + d)), acc);
+    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (lane == 0) p.zt[pair] = acc;
+}
+
 int warps_per_sm(int T) { return WARPS * (T > 4 ? 1 : 2); }
 
 template <typename E, int TG>
@@ -217,6 +249,17 @@ cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms,
     const int blocks = warps / WARPS;
     return dtype == SGEMM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, vec, blocks, dependent, stream)
                                      : launch_type<float>(p, vec, blocks, dependent, stream);
+}
+
+cudaError_t launch_vocab_few_targets(const VocabFewParams &p, int dtype, bool vec, bool dependent, cudaStream_t stream)
+{
+    const dim3 blocks((p.T * p.t.n + WARPS - 1) / WARPS);
+    if (dtype == SGEMM_DTYPE_BF16)
+        return launch_kernel(dependent, vec ? vocab_few_targets_kernel<__nv_bfloat16, true>
+                                            : vocab_few_targets_kernel<__nv_bfloat16, false>,
+                             blocks, dim3(WARPS * 32), 0, stream, p);
+    return launch_kernel(dependent, vec ? vocab_few_targets_kernel<float, true> : vocab_few_targets_kernel<float, false>,
+                         blocks, dim3(WARPS * 32), 0, stream, p);
 }
 
 }  // namespace sgemm_impl

@@ -48,7 +48,8 @@ struct VocabProblem {
 // What a call does, and the byte offsets of the parts of its workspace (those a call does not use are empty).
 struct VocabLayout {
     sgemm_vocab_plan_t pub;
-    bool few;      // a few tokens: vocab_few.cu, no parts
+    bool few;      // loss of a few tokens: vocab_few.cu, no parts
+    bool few_targets;  // gradients of as few: their logits at the targets from there too
     int ctas;      // CTAs per worker: 2 = pairs computing 256 x 256 tiles, 1 = 128 x 256
     int workers;
     bool split;           // FP32 operands, used as 16-bit parts
@@ -104,6 +105,9 @@ struct VocabFewParams {
 int vocab_few_warps(int T, int num_sms);
 cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms, bool dependent, cudaStream_t stream);
 
+// The products at the targets, before the scaling, into p.zt.
+cudaError_t launch_vocab_few_targets(const VocabFewParams &p, int dtype, bool vec, bool dependent, cudaStream_t stream);
+
 // Tile kernel (vocab_kernels.cu): one launch's tiles.
 enum VocabKind { kVocabLoss = 0, kVocabDz = 1, kVocabDw = 2, kVocabDh = 3 };
 
@@ -121,7 +125,7 @@ struct VocabTileParams {
     int z_kind, z_v0, z_tm, z_tn;
     int z_items;
     float2 *part;
-    float *zt;
+    float *zt;           // logits at the targets: left by the loss; read by dZ where a few tokens' products are there
     int stat_cols;       // pairs per token at part
     const float *lse, *dloss;
     int g_blocks;        // dZ's buffer: blocks of 64 entries per part, [parts][g_blocks][T][64]

@@ -545,10 +545,16 @@ __device__ __forceinline__ void make_dz(const VocabTileParams &p, float (&z)[COL
 #pragma unroll
         for (int i = 0; i < COLS; ++i) z[i] = i < cols ? z[i] : 0.0f;
     }
+    int last = -1;
     for_targets(p, r, row, c0, [&](int at) {
-        const float t = weight * r.q;
+        float keep = 1.0f, add = -weight * r.q;
+        if (p.zt != nullptr && at != last) {  // a few tokens: p of the logit that the loss had (vocab_few.cu)
+            keep = 0.0f;
+            add += g * exp2_approx(fminf(fmaf(p.zt[row * p.t.n + r.entry], p.scale * kLog2e, -L), l));
+            last = at;
+        }
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) z[i] -= i == at ? t : 0.0f;
+        for (int i = 0; i < COLS; ++i) z[i] = i == at ? fmaf(keep, z[i], add) : z[i];
     });
 }
 

@@ -75,6 +75,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
 
     const int few = f32 ? kFewTokensF32 : (q.align_flags & 3) == 3 ? kFewTokensBf16 : kFewTokensCopied;
     w.few = !grad && T <= few;
+    w.few_targets = grad && T <= few;
     w.split = f32 && !w.few;
     const int lines = T >= kLineTokens ? 5 : 1;  // the flags that spare H's copy; W's are the next bits
     w.copy_h = f32 ? w.split && q.dw : !w.few && (q.align_flags & lines) != lines;
@@ -94,6 +95,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.tlogq_off = take(T * q.n * 4);
     }
     int launches = (w.split ? 2 : w.copy_h + w.copy_w) + (q.n > 0);
+    if (w.few_targets) w.zt_off = take(T * std::max(1, q.n) * 4);
     if (!grad) {
         w.stat_cols = w.few ? vocab_few_warps(q.T, q.num_sms) : 2 * ((q.V + kVocabBN - 1) / kVocabBN);
         w.zt_off = take(T * std::max(1, q.n) * 4);
@@ -128,7 +130,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
             w.ldacc = round_up(q.D, 4);
             w.acc_off = take(w.dh_splits * T * w.ldacc * 4);
         }
-        launches = T > 0 ? launches + w.pub.pieces + 1 + q.dh : q.dw;
+        launches = T > 0 ? launches + w.few_targets + w.pub.pieces + 1 + q.dh : q.dw;
     }
     w.pub.launches = launches;
     w.pub.workspace_bytes = at;

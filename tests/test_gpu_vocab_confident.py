@@ -90,6 +90,13 @@ def test_sure_tokens(h, T, D, dtype):
     _check(h, *_sure_tokens(T, 1000, D, dtype))
 
 
-@pytest.mark.parametrize("T,dtype", [(200, BF16), (200, F32)])
+@pytest.mark.parametrize("T,dtype,pad", [(1, BF16, 0), (2, BF16, 0), (8, BF16, 1), (1, F32, 0), (8, F32, 0), (24, F32, 3)])
+@pytest.mark.parametrize("D", [1024, 4096])
+def test_few_sure_tokens(h, T, D, dtype, pad):
+    """Losses of a few tokens are accumulated in another way than their gradients' logits."""
+    _check(h, *_sure_tokens(T, 1000, D, dtype, pad))
+
+
+@pytest.mark.parametrize("T,dtype", [(200, BF16), (200, F32), (2, BF16), (20, F32)])
 def test_sure_tokens_of_a_distillation(h, T, dtype):
     _check(h, *_sure_tokens(T, 1000, 4096, dtype, level=128.0, gap=28.0), temperature=2.0)
