@@ -84,6 +84,7 @@ constexpr int kWarpStaging = 32 * 128;  // bytes: 32 rows of 128 (64 bfloat16 or
 constexpr float kLog2e = 1.4426950408889634f;                              // log2(e) in two FP32 parts
 constexpr float kLog2eLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 constexpr float kInf = __builtin_huge_valf();
+constexpr float kLeast = 1.40129846e-45f;  // the smallest positive FP32 number
 
 template <int CTAS>
 struct Shape {
@@ -496,7 +497,8 @@ __device__ __forceinline__ void leave_loss(const VocabTileParams &p, float (&z)[
         if (index_ok(row < p.T && r.entry >= 0 && r.entry < p.t.n, p.status, kWhereIdxVocabTarget))
             p.zt[row * p.t.n + r.entry] = r.scale * x;
     });
-    float k = r.scale * kLog2e;
+    // (not 0, which a tiny scale on a row of zeros would give: it must leave the columns past V at -infinity)
+    float k = fmaxf(r.scale * kLog2e, kLeast);
     const float top = k * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     const float base = top == -kInf ? 0.0f : -top;
     if (fabsf(base) >= kHugeLog2) {  // products rounded as M was

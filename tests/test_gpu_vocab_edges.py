@@ -1,0 +1,56 @@
+"""The vocabulary losses at scales, logits, masks and strides where a number or an
+argument leaves its range."""
+
+import math
+
+import pytest
+
+import dense_fp32_gemm_04_gb300 as sg
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import vocab_reference as vr  # noqa: E402
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def h():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dense_fp32_gemm_04_gb300 import _build
+
+    _build.build()
+    handle = sg.Sgemm(0)
+    yield handle
+    handle.close()
+
+
+def _problem(T, V, D, dtype, spread=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(T + V + D)
+    H = torch.randn(T, D, device="cuda", generator=gen).to(dtype)
+    W = (torch.randn(V, D, device="cuda", generator=gen) * spread / math.sqrt(D)).to(dtype)
+    return H, W, torch.randint(V, (T,), device="cuda", generator=gen), torch.randn(T, device="cuda", generator=gen) / T
+
+
+def _check(h, got, ref):
+    torch.cuda.synchronize()
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
+    for name, x in got.items():
+        vr.check(name, x, ref[name])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1e-9, 1e-30, 1e-38])
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_scales_so_small_that_logits_vanish(h, T, scale, dtype):
+    """Rows of zeros and of tiny numbers among others, a vocabulary that ends inside a tile: lse is log V."""
+    V, D = 700, 72
+    H, W, y, dloss = _problem(T, V, D, dtype)
+    H[1] = 0.0
+    H[2] = 1e-37
+    loss, lse = h.xent(H, W, y, scale=scale)
+    dH, dW = h.xent_grad(H, W, y, lse, dloss * (0.5 / scale), scale=scale)
+    ref = vr.reference(H, W, scale, 1.0, *vr.xent_targets(y, V), dloss.double() * (0.5 / scale), bf16=dtype == BF16)
+    _check(h, {"loss": loss, "lse": lse, "dH": dH, "dW": dW}, ref)
