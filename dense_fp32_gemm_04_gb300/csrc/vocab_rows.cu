@@ -18,7 +18,9 @@ using namespace sgemm_dev;
 
 constexpr float kInf = __builtin_huge_valf();
 
-// One block per token. q = softmax over the entries that count of logit * scale,
+// One block per token. q = softmax over the entries that count of logit * scale (of
+// the differences from the largest: a logit of the type's largest or lowest value
+// times a scale above 1 would leave FP32),
 // then the entries in ascending order of id: an entry's place is the number of
 // entries before it (n <= 1024, so n^2 comparisons in shared memory are less work
 // than the passes of a sort), equal ids staying in the given order. What is left
@@ -39,7 +41,7 @@ vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const floa
     for (int j = threadIdx.x; j < n; j += THREADS) {
         const long long id = ids[row * ldn + j];
         const bool counts = id >= 0 && id < V;
-        const float x = counts ? logits[row * ldn + j] * scale : -kInf;
+        const float x = counts ? logits[row * ldn + j] : -kInf;
         s_id[j] = counts && x > -kInf ? static_cast<int>(id) : kNoTarget;
         if (x != x) s_id[j] = static_cast<int>(id);  // a NaN logit stays and makes the token's loss NaN
         s_x[j] = x;
@@ -52,7 +54,7 @@ vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const floa
     for (int w = 1; w < THREADS / 32; ++w) best = fmaxf(best, s_red[0][w]);
     float sum = 0.0f;
     for (int j = threadIdx.x; j < n; j += THREADS)
-        if (s_id[j] != kNoTarget) sum += expf(s_x[j] - best);
+        if (s_id[j] != kNoTarget) sum += expf((s_x[j] - best) * scale);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_red[1][warp] = sum;
     __syncthreads();
@@ -64,7 +66,7 @@ vocab_targets_kernel(int V, int n, const long long *__restrict__ ids, const floa
         int at = 0;
         for (int i = 0; i < n; ++i) at += s_id[i] < id || (s_id[i] == id && i < j);
         const bool counts = id != kNoTarget;
-        const float t = s_x[j] - best;
+        const float t = (s_x[j] - best) * scale;
         tid[row * n + at] = id;
         tq[row * n + at] = counts ? expf(t) / sum : 0.0f;
         tlogq[row * n + at] = counts ? t - logsum : 0.0f;

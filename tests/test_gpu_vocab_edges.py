@@ -54,3 +54,25 @@ def test_scales_so_small_that_logits_vanish(h, T, scale, dtype):
     dH, dW = h.xent_grad(H, W, y, lse, dloss * (0.5 / scale), scale=scale)
     ref = vr.reference(H, W, scale, 1.0, *vr.xent_targets(y, V), dloss.double() * (0.5 / scale), bf16=dtype == BF16)
     _check(h, {"loss": loss, "lse": lse, "dH": dH, "dW": dW}, ref)
+
+
+@pytest.mark.parametrize("temperature", [0.25, 0.5, 1.0, 3.0])
+def test_teacher_logits_at_the_ends_of_their_type(h, temperature):
+    """Logits that a division by the temperature would take out of FP32: only their differences count."""
+    T, V, D, n = 40, 300, 32, 5
+    H, W, _, dloss = _problem(T, V, D, F32)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(V, (T, n), device="cuda", generator=gen)
+    logits = torch.randn(T, n, device="cuda", generator=gen)
+    far = torch.finfo(F32).max
+    logits[0] = -far  # masked by the type's lowest value throughout: a uniform teacher
+    logits[1, 1:] = -far  # one entry left
+    logits[2] = far
+    logits[3, :2], logits[3, 2:] = far, -far
+    logits[4] = -math.inf  # masked
+    logits[5, 1:] = -math.inf
+    logits[6] = 2e38
+    loss, lse = h.distill(H, W, ids, logits, temperature=temperature)
+    dH, dW = h.distill_grad(H, W, ids, logits, lse, dloss, temperature=temperature)
+    ref = vr.reference(H, W, 1 / temperature, temperature ** 2, *vr.teacher_targets(ids, logits, temperature, V), dloss)
+    _check(h, {"loss": loss, "lse": lse, "dH": dH, "dW": dW}, ref)
