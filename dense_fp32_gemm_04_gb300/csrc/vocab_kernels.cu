@@ -373,25 +373,43 @@ __device__ __forceinline__ void write_rows(const float (&acc)[COLS], float *stg,
     }
 }
 
+// Whether a token counts: it has a label, or a teacher's entry, in the vocabulary.
+__device__ __forceinline__ bool is_used(const VocabTileParams &p, long long row)
+{
+    if (row >= p.T) return false;
+    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
+    return p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
+}
+
 // dloss of a token, 0 for a masked one.
 __device__ __forceinline__ float load_dloss(const VocabTileParams &p, long long row)
 {
-    if (row >= p.T) return 0.0f;
-    const long long y = p.t.labels != nullptr ? p.t.labels[row] : p.t.id[row * p.t.n];
-    const bool used = p.t.labels != nullptr ? y >= 0 && y < p.V : y != kNoTarget;
-    return used ? p.dloss[row] : 0.0f;
+    return is_used(p, row) ? p.dloss[row] : 0.0f;
 }
 
-// dZ of bfloat16 operands is kept divided by the significand of dloss[0], a number in [1, 2), and dH and dW are multiplied
-// by it. The losses' gradients are mostly one number, 1 / tokens, and the label's entry of dZ that number times p - 1:
-// rounded as it is, all labels' entries would be off by much the same share; divided, it lies just below a power of two,
-// where bfloat16 is densest (mean loss of an untrained head, dH off by 1.68e-3 of its norm, which is the result's own
-// rounding; undivided 1.70e-3 over 1000 tokens, 1.99e-3 over 700, 2.43e-3 over 513).
-__device__ __forceinline__ float significand(const VocabTileParams &p)
+// dZ of bfloat16 operands is kept divided by the significand of the first dloss that counts, a number in [1, 2), and dH and
+// dW are multiplied by it. The losses' gradients are mostly one number, 1 / tokens, and the label's entry of dZ that number
+// times p - 1: rounded as it is, all labels' entries would be off by much the same share; divided, it lies just below a
+// power of two, where bfloat16 is densest (mean loss of an untrained head, dH off by 1.68e-3 of its norm, which is the
+// result's own rounding; undivided 1.70e-3 over 1000 tokens, 1.99e-3 over 700, 2.43e-3 over 513). Masked tokens may hold
+// anything, and a prompt is masked first: the warp looks past them, 256 tokens at a time, while the first tile's products
+// run.
+__device__ __forceinline__ float significand(const VocabTileParams &p, int lane)
 {
     if (p.dloss == nullptr) return 1.0f;
-    const uint32_t bits = __float_as_uint(load_dloss(p, 0)), exponent = bits >> 23 & 255u;  // a masked token's may be anything
-    return exponent == 0 || exponent == 255 ? 1.0f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    for (int t0 = 0; t0 < p.T; t0 += 256) {
+        bool used[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) used[j] = is_used(p, t0 + 32 * j + lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const unsigned some = __ballot_sync(0xffffffffu, used[j]);
+            if (some == 0) continue;
+            const uint32_t bits = __float_as_uint(p.dloss[t0 + 32 * j + __ffs(some) - 1]), exponent = bits >> 23 & 255u;
+            return exponent == 0 || exponent == 255 ? 1.0f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+        }
+    }
+    return 1.0f;
 }
 
 // What a thread needs to know of its row before the tile is there: fetched while the products run.
@@ -731,7 +749,7 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
     const int quarter = warp & 3, half = warp >> 3;
     unsigned char *area = staging + (warp - 4) * kWarpStaging;
     const uint32_t stg = smem_addr(area);
-    const float divide = F16 ? 1.0f : significand(p);
+    const float divide = F16 ? 1.0f : significand(p, lane);
     int it = 0;
     bool ok = true;
     Item w;

@@ -76,3 +76,31 @@ def test_teacher_logits_at_the_ends_of_their_type(h, temperature):
     dH, dW = h.distill_grad(H, W, ids, logits, lse, dloss, temperature=temperature)
     ref = vr.reference(H, W, 1 / temperature, temperature ** 2, *vr.teacher_targets(ids, logits, temperature, V), dloss)
     _check(h, {"loss": loss, "lse": lse, "dH": dH, "dW": dW}, ref)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("masked", [1, 187, 600])
+def test_the_mean_loss_after_a_masked_prompt(h, masked, op):
+    """The first tokens are masked, as a prompt is, and dloss is one number for all.
+
+    dZ held next to a power of two from below: off by at most 2^-7 / sqrt(12) / 1.98 = 1.1e-3 (2-norm), the result's
+    rounding 1.6e-3, 2.0e-3 together; held anywhere, by up to 2^-8 for all tokens alike. 1 / 513 lies just below a power
+    of two as well, so its rounding is the worst."""
+    T, V, D = 513 + masked, 5000, 256
+    H, W, y, _ = _problem(T, V, D, BF16, spread=0.5)
+    y[:masked] = -100
+    dloss = torch.full((T,), 1.0 / 513, device="cuda")
+    if op == "xent":
+        _, lse = h.xent(H, W, y)
+        dH, dW = h.xent_grad(H, W, y, lse, dloss)
+    else:
+        ids, logits = torch.where(y < 0, -1, y)[:, None].contiguous(), torch.zeros(T, 1, device="cuda")
+        _, lse = h.distill(H, W, ids, logits)
+        dH, dW = h.distill_grad(H, W, ids, logits, lse, dloss)
+    ref = vr.reference(H, W, 1.0, 1.0, *vr.xent_targets(y, V), dloss, bf16=True)
+    _check(h, {"dH": dH, "dW": dW}, ref)
+    for name, got in (("dH", dH), ("dW", dW)):
+        value = ref[name][0]
+        off = ((got.cpu().double() - value).norm() / value.norm()).item()
+        print(name, off)
+        assert off < 2.3e-3, name
