@@ -9,9 +9,13 @@ namespace sgemm_impl {
 
 namespace {
 
-// dZ of one piece of the vocabulary takes about this much at most (a piece is at least one tile wide), so that
-// two pieces' dZ stay a small part of the logits' size while a launch still has many rounds of tiles (training 4096
-// tokens, 131072 x 4096: the same time within 2 % from 128 MB to 1 GB).
+// dZ of the pieces of the vocabulary that are alive, in all the parts that are held of it, takes twice this much at most
+// (but a piece is at least one tile wide): the whole vocabulary in one piece where it fits that, else pieces of one size,
+// two of them alive at a time. A launch still has many rounds of tiles (training 4096 tokens, 131072 x 4096 in bfloat16:
+// the same time within 2 % with pieces of 128 MB to 1 GB; 2048 x 32768 x 2048 in FP32 2.71 ms with two pieces of 425 MB, 2.74
+// with three; 1000 x 32003 x 1001 738 us with one of 320 MB, 778 with two). Beside it a call holds what its operands and
+// dH's partial sums take, so for FP32, whose parts of W are as large as W, and for a few hundred tokens the workspace can be
+// larger than the logits would be.
 constexpr long long kPieceBytes = 256LL << 20;
 
 // Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
@@ -104,9 +108,16 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.pub.piece = q.V;
         launches = T > 0 ? launches + 2 : 0;
     } else {
-        const long long fit = std::max<long long>(kPieceBytes / (2 * w.parts) / std::max<long long>(T, 1), kVocabBN);
-        const long long most = q.piece > 0 ? round_up(q.piece, kVocabBN) : fit / kVocabBN * kVocabBN;
-        const long long piece = std::min<long long>(most, round_up(q.V, kVocabBN));
+        const int held = (q.dw || !w.split ? w.parts : 0) + (w.split && q.dh ? 2 : 0);  // for dW or both; float16 for dH
+        const long long column = 2LL * held * std::max<long long>(T, 1), all = round_up(q.V, kVocabBN);
+        long long piece = all;
+        if (q.piece > 0) {
+            piece = std::min(round_up(q.piece, kVocabBN), all);
+        } else if (all * column > 2 * kPieceBytes) {
+            const long long fit = std::max<long long>(kPieceBytes / column / kVocabBN, 1) * kVocabBN;
+            const long long pieces = (q.V + fit - 1) / fit;
+            piece = round_up((q.V + pieces - 1) / pieces, kVocabBN);
+        }
         w.pub.piece = static_cast<int>(std::min<long long>(piece, q.V));
         w.pub.pieces = static_cast<int>((q.V + piece - 1) / piece);
         w.g_blocks = static_cast<int>(piece / 64);
