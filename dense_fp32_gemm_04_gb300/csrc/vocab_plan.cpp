@@ -159,10 +159,13 @@ extern "C" int sgemm_vocab_plan(int T, int V, int D, int dtype, int n, int grad,
     const int rc = validate_vocab(q);
     if (rc != SGEMM_OK) return rc;
     *out = vocab_layout(q).pub;
-    if (grad != 0) {  // a call for one gradient alone splits its work differently: the workspace fits it too
-        for (bool dh : {false, true}) {
-            q.dh = dh;
-            q.dw = !dh;
+    // A call for one gradient alone splits its work differently, and so does one on a machine that holds no CTA pairs (fewer
+    // pairs than half the SMs split it less): the workspace fits them too.
+    for (int pairs : {0, -1}) {
+        q.pairs = pairs;
+        for (int one : {0, 1, 2}) {
+            q.dh = grad != 0 && one != 1;
+            q.dw = grad != 0 && one != 2;
             out->workspace_bytes = std::max(out->workspace_bytes, vocab_layout(q).pub.workspace_bytes);
         }
     }

@@ -145,7 +145,7 @@ typedef enum sgemm_option {
                                      an aligned workspace copy of C and copy it back */
     SGEMM_OPT_FORCE_VOCAB_PIECE = 12, /* vocabulary losses (sgemm_vocab.h): entries of the vocabulary per
                                      piece of a gradient call, rounded up to a multiple of 256 (0 =
-                                     automatic, the default) */
+                                     automatic, the default, and what sgemm_vocab_plan describes) */
     SGEMM_OPT_CLUSTER_SPLIT = 11  /* FP32 split-K: -1 = automatic (the default), 0 = partials
                                      always through the workspace and a reduction kernel, 1 =
                                      always within thread-block clusters when 2..8 splits (same

@@ -146,9 +146,12 @@ typedef struct sgemm_vocab_plan_s {
 /*
  * Host-only planning: what the calls above do on a GPU with `num_sms` SMs. n: 0
  * for the cross entropy, else the teacher's entries. grad: 0 for the loss, 1 for
- * the gradients (both of them; workspace_bytes is enough for either alone too).
+ * the gradients (both of them; workspace_bytes is enough for either alone too,
+ * and for any number of CTA pairs that the GPU holds at once).
  * align_flags: bit 0 = rows of H are 16-byte aligned (base and row stride), bit 1 =
- * rows of W, bits 2 and 3 = the same with 128 bytes. Needs no GPU.
+ * rows of W, bits 2 and 3 = the same with 128 bytes. Needs no GPU. The plan is
+ * that of automatic pieces: with SGEMM_OPT_FORCE_VOCAB_PIECE set on a handle, a call
+ * may need more workspace (one call outside a capture makes it large enough).
  */
 int sgemm_vocab_plan(int T, int V, int D, int dtype, int n, int grad, int align_flags,
                      int num_sms, int math_mode, sgemm_vocab_plan_t *out);
