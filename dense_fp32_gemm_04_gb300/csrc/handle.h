@@ -18,6 +18,7 @@ struct sgemm_handle_s {
     int num_sms = 0;
     int tf32_pairs = -1;  // CTA pairs of the TF32 pair kernel resident at once (-1: none fit)
     int vocab_pairs = -1; // the same for the vocabulary losses' kernel
+    bool vocab_ok = false; // that kernel can run (without it the other calls still do)
     int vocab_piece = 0;  // SGEMM_OPT_FORCE_VOCAB_PIECE
     int math_mode = SGEMM_MATH_FP32;
     int *d_status = nullptr;

@@ -461,8 +461,7 @@ int sgemm_create_for_device(int dev, sgemm_handle_t *out)
         return SGEMM_ERR_CUDA;
     }
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
-    if (ffma_set_attributes() != cudaSuccess || tf32_set_attributes() != cudaSuccess ||
-        vocab_set_attributes() != cudaSuccess) {
+    if (ffma_set_attributes() != cudaSuccess || tf32_set_attributes() != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return SGEMM_ERR_CUDA;
@@ -470,7 +469,9 @@ int sgemm_create_for_device(int dev, sgemm_handle_t *out)
     {
         const int pairs = tf32_pair_max_pairs();
         h->tf32_pairs = pairs > 0 ? std::min(pairs, sms / 2) : -1;
-        const int vocab = vocab_max_pairs();
+        h->vocab_ok = vocab_set_attributes() == cudaSuccess;
+        if (!h->vocab_ok) cudaGetLastError();
+        const int vocab = h->vocab_ok ? vocab_max_pairs() : 0;
         h->vocab_pairs = vocab > 0 ? std::min(vocab, sms / 2) : -1;
     }
     if (cudaMalloc(&h->d_status, 256) != cudaSuccess || cudaMemset(h->d_status, 0, 256) != cudaSuccess ||

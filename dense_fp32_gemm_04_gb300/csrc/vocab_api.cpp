@@ -73,6 +73,7 @@ int check(const Call &c, bool grad)
             return SGEMM_ERR_INVALID_VALUE;
     }
     if ((c.dH != nullptr && c.lddh < c.D) || (c.dW != nullptr && c.lddw < c.D)) return SGEMM_ERR_INVALID_VALUE;
+    if (!c.h->vocab_ok) return SGEMM_ERR_NOT_SUPPORTED;
     return SGEMM_OK;
 }
 

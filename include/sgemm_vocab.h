@@ -69,7 +69,8 @@
  * for a fixed shape, alignment and plan.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.
- * T, V or D so large that their tiles do not count in 32 bits: SGEMM_ERR_NOT_SUPPORTED.
+ * T, V or D so large that their tiles do not count in 32 bits, or kernels that this
+ * build or machine cannot run: SGEMM_ERR_NOT_SUPPORTED.
  * Device status (sgemm_check_device_status): the TF32 kernel's locations; in debug
  * builds also 35 the columns of dZ, 36 the softmax statistics, 37 the targets'
  * logits, 38 the rows of dW, 39 the splits of dH.

@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+import dense_fp32_gemm_04_gb300 as sg
 from conftest import ROOT
 
 CSRC = os.path.join(ROOT, "dense_fp32_gemm_04_gb300", "csrc")
@@ -43,3 +44,10 @@ def test_workspace_is_the_plans_whatever_is_resident(run, pairs, dtype):
             assert more == 0, (T, V, D, grads, more)
             if grads in (0, 3):
                 assert count == launches
+
+
+def test_a_handle_does_without_the_vocabulary_kernels(run):
+    """Where they cannot run, the GEMM does; the losses are refused and launch nothing."""
+    made, gemm, loss, grad, launched = run("attributes")
+    assert made == sg.SGEMM_OK and gemm == sg.SGEMM_OK
+    assert loss == grad == sg.SGEMM_ERR_NOT_SUPPORTED and launched == 0
