@@ -287,23 +287,30 @@ __device__ __forceinline__ void send_bf16(const CUtensorMap *map, float (&acc)[C
 // dZ for dH as two float16 parts, in blocks of 64 columns: columns times 2^15 factor[column] / most, which undoes the
 // scaling of W's row against the largest such factor, so that nothing leaves float16's range (dZ is at most 1 here).
 __device__ __forceinline__ void send_f16(const CUtensorMap *map, const float (&acc)[COLS],
-                                         const float *__restrict__ factor, float most, uint32_t stg, int lane, int x, int y,
+                                         const float *factor, float most, uint32_t stg, int lane, int x, int y,
                                          int blocks)
 {
     const float up = 1.0f / most;  // a power of two
 #pragma unroll
     for (int cb = 0; cb < COLS / 64; ++cb) {
+        const float4 *columns = reinterpret_cast<const float4 *>(factor + cb * 64);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
+            float4 next[2] = {columns[0], columns[1]};  // fetched one chunk ahead of its use
             stage_free(lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 uint32_t v[4];
+                const float4 now[2] = {next[0], next[1]};
+                if (j < 7) {
+                    next[0] = columns[2 * j + 2];
+                    next[1] = columns[2 * j + 3];
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float *f = acc + cb * 64 + 8 * j + 2 * i;
-                    const float2 u = __ldg(reinterpret_cast<const float2 *>(factor + cb * 64 + 8 * j + 2 * i));
-                    const float a = f[0] * (u.x * up * 32768.0f), b = f[1] * (u.y * up * 32768.0f);
+                    const float ux = i & 1 ? now[i / 2].z : now[i / 2].x, uy = i & 1 ? now[i / 2].w : now[i / 2].y;
+                    const float a = f[0] * (ux * up * 32768.0f), b = f[1] * (uy * up * 32768.0f);
                     __half2 y2 = __floats2half2_rn(a, b);
                     if (part == 1) {
                         const float2 back = __half22float2(y2);
@@ -481,12 +488,13 @@ __device__ __forceinline__ float (&columns(float (&acc)[COLS], int cb))[32]
     return reinterpret_cast<float(&)[32]>(acc[cb * 32]);
 }
 
-// Undo the scaling of W's rows (the same columns for every lane: broadcast loads).
-__device__ __forceinline__ void unscale_columns(const float *__restrict__ factor, float (&z)[COLS])
+// Undo the scaling of W's rows (the same columns for every lane: broadcast loads; plain ones, here and in send_f16: the call's
+// previous kernel wrote the factors while this one may already have been resident).
+__device__ __forceinline__ void unscale_columns(const float *factor, float (&z)[COLS])
 {
 #pragma unroll
     for (int i = 0; i < COLS; i += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(factor + i));
+        const float4 f = *reinterpret_cast<const float4 *>(factor + i);
         z[i] *= f.x;
         z[i + 1] *= f.y;
         z[i + 2] *= f.z;
@@ -824,14 +832,14 @@ __device__ __forceinline__ void leave_tiles(const VocabTileParams &p, Bars<Shape
             inside = inside && index_ok(c0 + COLS <= cols, p.status, kWhereIdxVocabDz);
             if (F16 && inside) {
                 if (p.dh_tm > 0)
-                    send_f16(&maps.Gzw, acc, p.w_unscale + p.z_v0 + c0, __ldg(p.w_most), stg, lane, c0, row, blocks);
+                    send_f16(&maps.Gzw, acc, p.w_unscale + p.z_v0 + c0, *p.w_most, stg, lane, c0, row, blocks);
                 if (p.dw_tn == 0) continue;
 #pragma unroll
                 for (int i = 0; i < COLS; ++i) acc[i] *= r.g;
             }
         } else if (w.kind == kVocabDh) {
             map = &maps.acc;
-            if (F16) alpha *= r.g * __ldg(p.w_most) * (1.0f / 32768.0f);
+            if (F16) alpha *= r.g * *p.w_most * (1.0f / 32768.0f);
             inside = inside && index_ok(w.split >= 0 && w.split < p.dh_splits, p.status, kWhereIdxVocabDh);
         } else {
             row = p.g_v0 + r0;

@@ -1,7 +1,9 @@
 // Row kernels of the vocabulary losses: the teacher's entries made into sorted
 // target tables, the losses put together from the tiles' partial softmax
 // statistics, and the end of the sum of dH. All of them are bound by a few
-// megabytes of traffic beside the products.
+// megabytes of traffic beside the products. What the call's previous kernel wrote is read
+// with plain loads: these kernels may be resident before it has ended, and the read-only
+// path is for memory that nobody writes meanwhile.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -94,8 +96,8 @@ __device__ __forceinline__ void fold(float &m, float &s, float m2, float s2)
 
 template <int ROWS>
 __global__ void __launch_bounds__(kCombineThreads)
-vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ part, int parts,
-                     const float *__restrict__ zt, float mult, float *__restrict__ loss, float *__restrict__ lse)
+vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *part, int parts, const float *zt, float mult, float *loss,
+                     float *lse)
 {
     constexpr int LANES = kCombineThreads / ROWS;
     __shared__ float sm[LANES][ROWS + 1], ss[LANES][ROWS + 1];
@@ -152,7 +154,7 @@ vocab_combine_kernel(int T, int V, VocabTargets t, const float2 *__restrict__ pa
 // block per row and 1024 columns; bound by the sums' bytes (4096 x 4096, one split: 26 us; ldacc is a multiple of 4).
 template <typename E>
 __global__ void __launch_bounds__(256)
-vocab_finish_kernel(int cols, const float *__restrict__ acc, long long ldacc, long long split, int splits, float beta,
+vocab_finish_kernel(int cols, const float *acc, long long ldacc, long long split, int splits, float beta,
                     E *__restrict__ dst, long long ldd)
 {
     const long long r = blockIdx.x;
