@@ -222,20 +222,23 @@ __global__ void __launch_bounds__(WARPS * 32) vocab_few_targets_kernel(const Voc
 
 int warps_per_sm(int T) { return WARPS * (T > 4 ? 1 : 2); }
 
-template <typename E, int TG>
-cudaError_t launch(const VocabFewParams &p, bool vec, int blocks, bool dependent, cudaStream_t stream)
+template <typename E, int TG, bool VEC>
+cudaError_t launch(const VocabFewParams &p, int blocks, bool dependent, cudaStream_t stream)
 {
-    return launch_kernel(dependent, vec ? vocab_few_kernel<E, TG, true> : vocab_few_kernel<E, TG, false>, dim3(blocks),
-                         dim3(WARPS * 32), 0, stream, p);
+    return launch_kernel(dependent, vocab_few_kernel<E, TG, VEC>, dim3(blocks), dim3(WARPS * 32), 0, stream, p);
 }
 
-template <typename E>
-cudaError_t launch_type(const VocabFewParams &p, bool vec, int blocks, bool dependent, cudaStream_t stream)
+// MOST: tokens that a call of this type and alignment can have here (vocab_plan.cpp).
+template <typename E, bool VEC, int MOST>
+cudaError_t launch_tokens(const VocabFewParams &p, int blocks, bool dependent, cudaStream_t stream)
 {
-    if (p.T > 4) return launch<E, 8>(p, vec, blocks, dependent, stream);
-    if (p.T > 2) return launch<E, 4>(p, vec, blocks, dependent, stream);
-    if (p.T > 1) return launch<E, 2>(p, vec, blocks, dependent, stream);
-    return launch<E, 1>(p, vec, blocks, dependent, stream);
+    if (p.T > MOST) return cudaErrorInvalidValue;
+    if constexpr (MOST > 4)
+        if (p.T > 4) return launch<E, 8, VEC>(p, blocks, dependent, stream);
+    if constexpr (MOST > 2)
+        if (p.T > 2) return launch<E, 4, VEC>(p, blocks, dependent, stream);
+    if (p.T > 1) return launch<E, 2, VEC>(p, blocks, dependent, stream);
+    return launch<E, 1, VEC>(p, blocks, dependent, stream);
 }
 
 }  // namespace
@@ -247,8 +250,11 @@ cudaError_t launch_vocab_few(VocabFewParams p, int dtype, bool vec, int num_sms,
     const int warps = vocab_few_warps(p.T, num_sms);
     p.rows = (p.V + warps - 1) / warps;
     const int blocks = warps / WARPS;
-    return dtype == SGEMM_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, vec, blocks, dependent, stream)
-                                     : launch_type<float>(p, vec, blocks, dependent, stream);
+    if (dtype == SGEMM_DTYPE_BF16)
+        return vec ? launch_tokens<__nv_bfloat16, true, kFewTokensBf16>(p, blocks, dependent, stream)
+                   : launch_tokens<__nv_bfloat16, false, kFewTokensCopied>(p, blocks, dependent, stream);
+    return vec ? launch_tokens<float, true, kFewTokensF32>(p, blocks, dependent, stream)
+               : launch_tokens<float, false, kFewTokensF32>(p, blocks, dependent, stream);
 }
 
 cudaError_t launch_vocab_few_targets(const VocabFewParams &p, int dtype, bool vec, bool dependent, cudaStream_t stream)

@@ -30,6 +30,12 @@ struct VocabTargets {
     const float *logq;        // [T][n]
 };
 
+// Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
+// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 82 / 281, 24
+// tokens 230 / 281, 32 tokens 302 / 281; bfloat16 131072 x 4096, 2 tokens 164 / 172, 3 tokens 290 / 173; rows at an odd
+// stride, 50021 x 1531, 8 tokens 87 / 92, 12 tokens 165 / 92.
+constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
+
 // Tile shape: 256 columns per tile, slabs of 64 along K; 128 rows per CTA.
 constexpr int kVocabBN = 256, kVocabBK = 64;
 

@@ -18,12 +18,6 @@ namespace {
 // larger than the logits would be.
 constexpr long long kPieceBytes = 256LL << 20;
 
-// Losses of up to this many tokens run without tensor cores (vocab_few.cu); `copied`: bfloat16 rows that the tensor
-// cores would need copied first. Measured, us without / with tensor cores: FP32 50021 x 2048, 8 tokens 82 / 281, 24
-// tokens 230 / 281, 32 tokens 302 / 281; bfloat16 131072 x 4096, 2 tokens 164 / 172, 3 tokens 290 / 173; rows at an odd
-// stride, 50021 x 1531, 8 tokens 87 / 92, 12 tokens 165 / 92.
-constexpr int kFewTokensF32 = 24, kFewTokensBf16 = 2, kFewTokensCopied = 8;
-
 // From this many tokens on bfloat16 rows that do not start on 128-byte lines are copied to rows that do, though the copy
 // engine could read them: a slab's row is then one line and not parts of two (50000 x 1496, loss in us, read as they are
 // / with the copies: 2048 tokens 242 / 232, 4096 tokens 446 / 399; gradients 589 / 590 and 1155 / 1110; with rows on
