@@ -180,9 +180,10 @@ int begin(const Call &c, const VocabLayout &w, VocabTileParams *p, VocabMaps *m)
     return SGEMM_OK;
 }
 
-VocabFewParams few_params(const Call &c, const VocabTileParams &p)
+VocabFewParams few_params(const Call &c, const VocabLayout &w, const VocabTileParams &p)
 {
-    return VocabFewParams{c.T, c.V, c.D, c.H, c.W, c.ldh, c.ldw, c.scale, p.t, p.part, p.zt, 0, c.h->d_status};
+    return VocabFewParams{c.T,    c.V,  c.D,         c.H,       c.W, c.ldh,       c.ldw, c.scale, p.t,
+                          p.part, p.zt, w.stat_cols, w.targets, 0,   c.h->d_status};
 }
 
 bool few_vec(const Call &c) { return (problem(c).align_flags & 3) == 3; }
@@ -210,7 +211,7 @@ int run_loss(const Call &c)
     p.zt = reinterpret_cast<float *>(ws + w.zt_off);
     p.stat_cols = w.stat_cols;
     if (w.few) {
-        const VocabFewParams f = few_params(c, p);
+        const VocabFewParams f = few_params(c, w, p);
         if (launch_vocab_few(f, c.dtype, few_vec(c), c.h->num_sms, c.dependent(), c.stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
     } else if (launch_vocab_tiles(m, p, w.ctas, w.workers, c.dependent(), c.stream) != cudaSuccess) {
         return SGEMM_ERR_LAUNCH;
@@ -241,7 +242,7 @@ int run_grad(const Call &c)
     if ((rc = begin(c, w, &p, &m)) != SGEMM_OK) return rc;
     if (w.few_targets) {
         p.zt = reinterpret_cast<float *>(ws + w.zt_off);
-        if (launch_vocab_few_targets(few_params(c, p), c.dtype, few_vec(c), c.dependent(), c.stream) != cudaSuccess)
+        if (launch_vocab_few_targets(few_params(c, w, p), c.dtype, few_vec(c), c.dependent(), c.stream) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
     }
     const int bm = 128 * w.ctas, tm = ceil_div(c.T, bm), tn = ceil_div(c.D, kVocabBN);

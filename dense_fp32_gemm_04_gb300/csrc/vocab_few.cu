@@ -171,19 +171,19 @@ __global__ void __launch_bounds__(WARPS * 32, TG > 4 ? 1 : 2) vocab_few_kernel(c
             m = top;
             if (p.t.labels != nullptr) {
                 const long long y = p.t.labels[token];
-                if (y >= v && y < v + rows && index_ok(token < p.T, p.status, kWhereIdxVocabTarget))
+                if (y >= v && y < v + rows && index_ok(token < p.targets, p.status, kWhereIdxVocabTarget))
                     p.zt[token] = p.scale * sums[warp][lane * R + static_cast<int>(y - v)];
             } else {
                 const long long list = static_cast<long long>(token) * p.t.n;
                 for (; entry < p.t.n; ++entry) {
                     const int y = p.t.id[list + entry];
                     if (y >= v + rows) break;  // kNoTarget ends the list too
-                    if (index_ok(y >= v, p.status, kWhereIdxVocabTarget))
+                    if (index_ok(y >= v && list + entry < p.targets, p.status, kWhereIdxVocabTarget))
                         p.zt[list + entry] = p.scale * sums[warp][lane * R + y - v];
                 }
             }
         }
-        if (mine && index_ok(gw < static_cast<int>(gridDim.x) * WARPS, p.status, kWhereIdxVocabStat))
+        if (mine && index_ok(gw < p.stat_rows, p.status, kWhereIdxVocabStat))
             p.part[static_cast<long long>(gw) * p.T + token] = make_float2(m, s);
     }
 }
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(WARPS * 32) vocab_few_targets_kernel(const Voc
     for (int d = whole + lane; d < p.D; d += 32)
         acc = fmaf(static_cast<float>(__ldg(w + d)), static_cast<float>(__ldg(h + d)), acc);
     for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (lane == 0) p.zt[pair] = acc;
+    if (lane == 0 && index_ok(pair < p.targets, p.status, kWhereIdxVocabTarget)) p.zt[pair] = acc;
 }
 
 int warps_per_sm(int T) { return WARPS * (T > 4 ? 1 : 2); }

@@ -68,6 +68,7 @@ struct VocabLayout {
     long long gz_off[2];                   // dZ of a piece in float16 parts for dH, [2][g_blocks][T][64]
     long long tid_off, tq_off, tlogq_off;  // target tables [T][n]
     long long zt_off;                      // logits at the targets, [T][n]
+    int targets;                           // of them, for a few tokens
     long long part_off;                    // (max, sum of exp) per token and 128 columns or warp, [stat_cols][T]
     int stat_cols;                         // pairs per token
     long long g_off[2];                    // dZ of a piece, [parts][g_blocks][T][64]; two of them, in turn
@@ -103,8 +104,9 @@ struct VocabFewParams {
     long long ldh, ldw;
     float scale;
     VocabTargets t;
-    float2 *part;  // [vocab_few_warps][T]
-    float *zt;
+    float2 *part;  // [stat_rows][T]
+    float *zt;     // [targets]
+    int stat_rows, targets;  // what the workspace has room for (for the debug build's checks)
     int rows;  // of the vocabulary per warp (set by the launch)
     int *status;
 };

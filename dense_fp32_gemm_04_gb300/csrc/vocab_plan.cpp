@@ -93,6 +93,7 @@ VocabLayout vocab_layout(const VocabProblem &q)
         w.tlogq_off = take(T * q.n * 4);
     }
     int launches = (w.split ? 2 : w.copy_h + w.copy_w) + (q.n > 0);
+    if (w.few || w.few_targets) w.targets = static_cast<int>(T * std::max(1, q.n));
     if (w.few_targets) w.zt_off = take(T * std::max(1, q.n) * 4);
     if (!grad) {
         w.stat_cols = w.few ? vocab_few_warps(q.T, q.num_sms) : 2 * ((q.V + kVocabBN - 1) / kVocabBN);

@@ -105,8 +105,16 @@ cudaError_t launch_vocab_finish(int, int, const float *, long long, long long, i
 {
     return launched();
 }
-cudaError_t launch_vocab_few(VocabFewParams, int, bool, int, bool, cudaStream_t) { return launched(); }
-cudaError_t launch_vocab_few_targets(const VocabFewParams &, int, bool, bool, cudaStream_t) { return launched(); }
+// What the debug build's checks hold the few-token kernels to is what they write: a launch that says otherwise fails.
+cudaError_t launch_vocab_few(VocabFewParams p, int, bool, int num_sms, bool, cudaStream_t)
+{
+    const bool good = p.stat_rows == vocab_few_warps(p.T, num_sms) && p.targets == p.T * p.t.n;
+    return good ? launched() : cudaErrorInvalidValue;
+}
+cudaError_t launch_vocab_few_targets(const VocabFewParams &p, int, bool, bool, cudaStream_t)
+{
+    return p.targets == p.T * p.t.n ? launched() : cudaErrorInvalidValue;
+}
 cudaError_t launch_vocab_tiles(const VocabMaps &, const VocabTileParams &, int, int, bool, cudaStream_t) { return launched(); }
 cudaError_t launch_vocab_copy(const void *, long long, int, int, void *, long long, bool, cudaStream_t) { return launched(); }
 cudaError_t launch_vocab_split(const void *, long long, int, int, void *, float *, int, float *, float *, void *, int,

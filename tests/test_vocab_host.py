@@ -36,7 +36,7 @@ def run(tmp_path_factory):
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_workspace_is_the_plans_whatever_is_resident(run, pairs, dtype):
     """Fewer CTA pairs than half the SMs, or none, need no more workspace than sgemm_vocab_plan gives: a captured call fits."""
-    for T, V, D in ((400, 32768, 1024), (700, 50021, 513), (2000, 32768, 2048), (4096, 131072, 256), (8, 5000, 64),
+    for T, V, D in ((400, 32768, 1024), (700, 50021, 513), (2000, 32768, 2048), (4096, 131072, 256), (8, 5000, 64), (1, 300, 40),
                     (300, 9000, 4096), (600, 32768, 1024), (1100, 32768, 2048)):
         for grads in (0, 1, 2, 3):
             made, planned, reserved, rc, more, launches, count = run("workspace", pairs, T, V, D, dtype, grads)
