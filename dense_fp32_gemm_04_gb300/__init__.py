@@ -205,6 +205,14 @@ def configs():
     return out
 
 
+def _int_args(name, rows, cols, ld):
+    """Refuse what the C entry points' int arguments would cut to its lower 32 bits."""
+    if max(rows, cols) >= 2 ** 31:
+        raise ValueError(f"{name} has {rows} x {cols} elements: sizes are 32-bit")
+    if ld >= 2 ** 31:
+        raise ValueError(f"{name} has a row stride of {ld} elements: strides are 32-bit")
+
+
 def _matrix_arg(t, rows, cols, name):
     """(pointer, leading dimension) of a row-major 2-D float32 CUDA tensor."""
     import torch
@@ -218,6 +226,7 @@ def _matrix_arg(t, rows, cols, name):
     if rows > 0 and cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
     ld = t.stride(0) if rows > 1 else max(1, cols)
+    _int_args(name, rows, cols, ld)
     return t.data_ptr(), max(ld, 1)
 
 
@@ -235,7 +244,9 @@ def _rows_arg(t, rows, cols, name, like=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     if rows > 0 and cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else max(1, cols))
+    ld = t.stride(0) if rows > 1 else max(1, cols)
+    _int_args(name, rows, cols, ld)
+    return t.data_ptr(), ld
 
 
 def _list_arg(t, shape, dtype, name, like):
@@ -252,7 +263,9 @@ def _list_arg(t, shape, dtype, name, like):
         return t.data_ptr()
     if shape[0] > 0 and shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else max(1, shape[1]))
+    ld = t.stride(0) if shape[0] > 1 else max(1, shape[1])
+    _int_args(name, *shape, ld)
+    return t.data_ptr(), ld
 
 
 class Sgemm:

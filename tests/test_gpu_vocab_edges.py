@@ -104,3 +104,21 @@ def test_the_mean_loss_after_a_masked_prompt(h, masked, op):
         off = ((got.cpu().double() - value).norm() / value.norm()).item()
         print(name, off)
         assert off < 2.3e-3, name
+
+
+def test_row_strides_past_32_bits_are_refused(h):
+    """The C entry points take strides as int: one that does not fit is an error, not its lower bits."""
+    D = 8
+    far = torch.empty(2 ** 32 + 2 * D, device="cuda", dtype=BF16).as_strided((2, D), (2 ** 32 + D, 1))
+    near, y = torch.zeros(3, D, device="cuda", dtype=BF16), torch.zeros(3, device="cuda", dtype=torch.int64)
+    lse = torch.zeros(3, device="cuda")
+    with pytest.raises(ValueError, match="row stride"):
+        h.xent(near, far, y)
+    with pytest.raises(ValueError, match="row stride"):
+        h.xent(far, near, y[:2])
+    with pytest.raises(ValueError, match="row stride"):
+        h.xent_grad(near[:2], near, y[:2], lse[:2], lse[:2], dH=far)
+    with pytest.raises(ValueError, match="row stride"):
+        h.xent_grad(near, near[:2], y, lse, lse, dW=far)
+    del far
+    torch.cuda.empty_cache()
