@@ -14,7 +14,8 @@
 // Bound by W's bytes up to 4 tokens (1 token x 131072 x 4096: bfloat16 158 us the
 // call, FP32 301 us the kernel, 7.1 TB/s; FP32, 50021 x 2048, 4 tokens 62 us, 6.6
 // TB/s), then by the latency of the loads at the 8 warps per
-// SM that R * TG sums leave room for (8 tokens 76 us, 16 tokens 147). Sums of 16
+// SM that R * TG sums leave room for (8 tokens 76 us, 16 tokens 147). The FP32 form for 4
+// tokens spills 120 bytes a thread at the 128 registers of two blocks per SM. Sums of 16
 // tokens, R of 4, packed FP32 and H in shared memory measured the same or slower.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -230,7 +230,9 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4])
 }
 
 // alpha * FP32 columns, 32 per block. (Scaling here and not in dZ also lets the stores' groups of four registers be
-// others than the accumulator's: without it the kernel spills 60 of them.)
+// others than the accumulator's: without it the kernel spills 60 of them. As it is, a thread spills 44 and 28 bytes in the
+// bfloat16 forms, single CTAs and pairs, 136 and 96 in the FP32 ones; between tiles and in their epilogue, where 128 of
+// its 216 registers are the tile.)
 __device__ __forceinline__ void send_f32(const CUtensorMap *map, const float (&acc)[COLS], uint32_t stg, int lane, int x,
                                          int y, int z, int cols, bool add, float alpha)
 {

@@ -55,7 +55,8 @@
  * that cancels in exp(Z - lse); dH and dW of FP32 operands are accumulated 256
  * deep (sums over terms of one sign, which lose most: dH 2.3e-6, dW 1e-7 of
  * themselves, the others 4e-7 to 8e-7). (Losses of a few tokens do without tensor cores;
- * their gradients take the logits at the targets in the same way.) bfloat16 operands
+ * their gradients take the logits at the targets in the same way.) FP32 Z overflows
+ * where D max |W| is 5e33 and more, however small H. bfloat16 operands
  * enter the products as they are and dZ enters them rounded to bfloat16; dH and
  * dW are rounded once. FP32 operands enter the tensor cores as sums of 16-bit
  * parts: for the logits and dH two float16 parts (22 bits) of rows scaled by
