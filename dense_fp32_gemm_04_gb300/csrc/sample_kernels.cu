@@ -161,10 +161,12 @@ struct Weigh {
         const f2 dl = add_f32x2(fma_f32x2(rest1, less, l), fma_f32x2(back, less, both(-top)));
         const f2 tm = mul_f32x2(dh, both(-ch));  // -t
         const f2 tl = add_f32x2(fma_f32x2(dh, c, tm), fma_f32x2(dh, both(cl), mul_f32x2(dl, c)));
-        // Below 2^-60 (and where l is -infinity or NaN) the bits of w are shifted out, whatever they are.
+        // Below 2^-(60 - drop) (and where l is -infinity or NaN) the bits of w are shifted out, whatever they are: by 60, as a
+        // shift by 64 would leave them all.
         float t0, t1;
         unpack_f32x2(tm, t0, t1);
-        const f2 th = pack_f32x2(fmaxf(-t0, -60.0f), fmaxf(-t1, -60.0f));
+        const float far = static_cast<float>(drop - 60);
+        const f2 th = pack_f32x2(fmaxf(-t0, far), fmaxf(-t1, far));
         // t = k / 1024 + r, r at most 2^-11 and a little
         constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: its neighbours are 1 apart, k stands in its low bits
         constexpr int kBits = 0x4b400000;

@@ -29,10 +29,11 @@
  *     below 0 is 0 and one that is not below 1 is off, a min_p that is not above 0 is off and one above 1
  *     is 1. u is read as 0 where it is not above 0, and u >= 1 takes the last kept entry of weight.
  *
- * Numerics: weights are held to 2^-44 of the largest one (fewer bits from 2^18 entries on, so that the sum of V of
- * them fits 64 bits) and summed exactly, as integers. Tokens and cuts are
- * so those of the formulas in 64-bit floating point, but for borders that lie within about 2^-37 of u S or of
- * top_p's share; the result does not depend on the order of sums or on the launch. logp is off by at most 2.5 * 2^-22 + 2^-22 |logp|.
+ * Numerics: weights are held to a unit of 2^-44 of the largest one (2^-(44 - d) for vocabularies of 2^18 to 2^(18 + d)
+ * entries, so that the sum of V of them fits 64 bits) and summed exactly, as integers. Tokens and cuts are
+ * so those of the formulas, but for borders that lie nearer to u S or to top_p's share than the roundings add up to: V
+ * units at the very worst, some sqrt(V) as a rule. The result does not depend on the order of sums or on the launch.
+ * logp is off by at most 2.5 * 2^-22 + 2^-22 |logp| and what its token's unit and those of S are of them.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.
  * CUDA graphs: a call may be captured at any time.
