@@ -1281,7 +1281,7 @@ sample_kernel(const SampleParams p)
     const float top_p = p.how.top_ps != nullptr ? p.how.top_ps[r] : p.how.top_p;
     const float min_p0 = p.how.min_ps != nullptr ? p.how.min_ps[r] : p.how.min_p;
     const float u = p.u[r];
-    t.tau = tau0 > 0.0f ? tau0 : 0.0f;
+    t.tau = tau0 > 0.0f ? fminf(tau0, 3.402823466e38f) : 0.0f;  // (0 times infinity would be no weight at all)
     // log2(e) / T in two parts (below 2^-127 a temperature counts as that: logits that differ by less than 1e-37 would show it)
     constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);
     const float divide = t.tau > 0.0f ? fmaxf(t.tau, 5e-39f) : 1.0f;

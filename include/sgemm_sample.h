@@ -25,9 +25,10 @@
  *     have weight, 1 each. A mask of the type's lowest value is an entry like others: far
  *     below the rest it has no weight, alone it is uniform.
  *   - The arrays of `how` hold one value per row, and a value that the call could not
- *     refuse is read so: a temperature that is not above 0 is 0, a top_k below 1 is off, a top_p
- *     below 0 is 0 and one that is not below 1 is off, a min_p that is not above 0 is off and one above 1
- *     is 1. u is read as 0 where it is not above 0, and u >= 1 takes the last kept entry of weight.
+ *     refuse is read so: a temperature that is not above 0 is 0 and an infinite one FP32's largest
+ *     number, a top_k below 1 is off, a top_p below 0 is 0 and one that is not below 1 is off, a min_p
+ *     that is not above 0 is off and one above 1 is 1. u is read as 0 where it is not above 0, and
+ *     u >= 1 takes the last kept entry of weight.
  *
  * Numerics: weights are held to a unit of 2^-44 of the largest one (2^-(44 - d) for vocabularies of 2^18 to 2^(18 + d)
  * entries, so that the sum of V of them fits 64 bits) and summed exactly, as integers. Tokens and cuts are
