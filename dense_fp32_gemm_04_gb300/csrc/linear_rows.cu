@@ -186,14 +186,16 @@ linear_columns_kernel(int N, int strips, const float *sums, float beta, E *db, c
     if (most != nullptr) unscale[c] = unscale_of(y);
 }
 
-// A scaled value as two float16 numbers (22 bits); infinities and NaN stay in the first.
-__device__ __forceinline__ void two_halves(const float (&x)[2], __half *to, long long part, bool second)
+// Two scaled values as two float16 numbers each (22 bits). The first is finite and what is left, infinities and NaN too, is in the
+// second: that only meets the other operand's first number, whose sign and zero are the operand's, so an infinity gives what the
+// formula has. (In the first one it would also meet the other operand's second number, which may be 0 or of the other sign.)
+__device__ __forceinline__ void two_halves(const float (&x)[2], __half *to, long long part)
 {
-    __half2 hi = __floats2half2_rn(x[0], x[1]);
+    const __half2 most = __float2half2_rn(65504.0f);  // the largest float16
+    const __half2 hi = __hmax2(__hmin2(__floats2half2_rn(x[0], x[1]), most), __hneg2(most));
     const float2 back = __half22float2(hi);
-    float lo[2] = {fabsf(x[0]) < kInf ? x[0] - back.x : 0.0f, second && fabsf(x[1]) < kInf ? x[1] - back.y : 0.0f};
     *reinterpret_cast<__half2 *>(to) = hi;
-    *reinterpret_cast<__half2 *>(to + part) = __floats2half2_rn(lo[0], lo[1]);
+    *reinterpret_cast<__half2 *>(to + part) = __floats2half2_rn(x[0] - back.x, x[1] - back.y);
 }
 
 // FP32 rows x = src (* slope) as float16 parts, a block per row. by_row: x times factor[column] (if given), scaled for each row
@@ -272,11 +274,11 @@ linear_parts_kernel(int rows, int cols, const float *__restrict__ src, long long
             float f[2];
             factors(c, f);
             const float y[2] = {v[0] * f[0] * up, v[1] * f[1] * up};
-            two_halves(y, by_row + r * ldp + c, part, second);
+            two_halves(y, by_row + r * ldp + c, part);
         }
         if (by_column != nullptr) {
             const float y[2] = {v[0] * inverse_power(column_unscale[c]), second ? v[1] * inverse_power(column_unscale[c + 1]) : 0.0f};
-            two_halves(y, by_column + r * ldp + c, part, second);
+            two_halves(y, by_column + r * ldp + c, part);
         }
     };
 #pragma unroll

@@ -1,0 +1,92 @@
+"""Linear layers over the whole range of their types: infinities, results next to FP32's ends, operands of very different sizes,
+deep sums, and how exact FP32 results are.
+
+Bounds for FP32 operands, per element of a product of a and b, mag = sum |a||b| over K: an operand is two float16 numbers, so it
+is off by 2^-23 of itself, or by 2^-39 of the largest of its row (2^-25, half the last place of a float16 below 2^-14, where that
+largest one lies in [2^14, 2^16)); the product of the two small parts, at most 2^-22 of |a||b|, is left out; sums of 256 products
+are 16 truncations for each of three products of parts, 48 * 2^-23 at most, and K / 256 of them are added in FP32. All together
+2^-17 mag, K 2^-24 mag and 2^-38 (largest |a| of the row * sum |b| + largest |b| * sum |a|). As a whole results are far nearer:
+truncations of 2^-24 on average, of sums that grow from 0, come to 24 * 2^-25 = 2^-20.4 of a sum of one sign, and to less of
+random signs, whose sums are some sqrt(K) of their terms while the parts' errors are as random as they are.
+"""
+
+import itertools
+import math
+
+import pytest
+
+import dense_fp32_gemm_04_gb300 as sg
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+BF16, F32 = torch.bfloat16, torch.float32
+# few tokens, tiles split over clusters, whole tiles
+FORMS = [(3, 300, 200), (150, 520, 200), (2200, 2400, 192)]
+
+
+@pytest.fixture(scope="module")
+def h():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    handle = sg.Sgemm(0)
+    yield handle
+    handle.close()
+
+
+def rand(gen, *shape):
+    return torch.randn(*shape, device="cuda", generator=gen)
+
+
+def off(a, b, dtype):
+    """What a product of the rows of a and b may be off by before it is rounded (infinities and NaN taken as 0)."""
+    a, b = (x.double().nan_to_num(nan=0.0, posinf=0.0, neginf=0.0).abs() for x in (a, b))
+    K, mag = a.shape[1], a @ b.T
+    tol = mag * ((K + 32) * 2.0 ** -24 + 2.0 ** -17)
+    if dtype == F32:
+        tol += 2.0 ** -38 * (a.max(1, keepdim=True).values * b.sum(1) + a.sum(1, keepdim=True) * b.max(1).values)
+    return tol
+
+
+def same(got, want, tol, dtype):
+    """Equal where want is infinite or NaN, else within tol and a rounding; results next to FP32's end may be on either side of it."""
+    most = torch.finfo(dtype).max
+    got = got.double()
+    half = torch.finfo(dtype).eps / 2
+    near = (got - want).abs() <= tol + half * (want.abs() + tol) + 2.0 ** -149
+    past = (want.abs() + tol >= most) & (got.isinf() | near) & (got.sign() == want.sign())
+    inf = want.isinf() & (got == want)
+    return bool((near | past | inf | (want.isnan() & got.isnan())).all())
+
+
+def product(a, b):
+    """The rows of a times those of b in 64 bits, with infinities and NaN as the formula has them whatever the library does."""
+    clean = [x.double().nan_to_num(nan=0.0, posinf=0.0, neginf=0.0) for x in (a, b)]
+    ref = clean[0] @ clean[1].T
+    rows = (~a.isfinite()).any(1).nonzero()[:, 0].tolist()
+    cols = (~b.isfinite()).any(1).nonzero()[:, 0].tolist()
+    for r in rows:
+        ref[r] = (a[r].double() * b.double()).sum(1)
+    for c in cols:
+        ref[:, c] = (a.double() * b[c].double()).sum(1)
+    return ref
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_infinite_operands(h, M, N, K, dtype):
+    """An infinity gives what the formula has: infinite results of its sign times the other operand's, NaN beside a zero."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    X, W, dY = rand(gen, M, K).to(dtype), rand(gen, N, K).to(dtype), rand(gen, M, N).to(dtype)
+    X[1, 7], X[2, 9], W[5, 11], W[N - 1, K - 1] = math.inf, -math.inf, math.inf, -math.inf
+    X[0, 11], W[17, 7] = math.inf, 0.0        # two infinities meet, and one meets a zero
+    W[40, :] = torch.tensor(1.5).to(dtype)    # numbers that one part holds
+    dY[1, 3], dY[M - 1, 6], dY[2, 17], X[2, 4] = math.inf, -math.inf, math.inf, 0.0
+    Y = h.linear(X, W)
+    dX, dW, _ = h.linear_grad(X, W, dY, need_db=False)
+    torch.cuda.synchronize()
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
+    for got, a, b in ((Y, X, W), (dX, dY, W.T), (dW, dY.T, X.T)):
+        want = product(a, b)
+        assert want.isinf().any() and want.isnan().any()
+        assert same(got, want, off(a, b, dtype), dtype)
