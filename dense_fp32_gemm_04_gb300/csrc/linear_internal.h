@@ -48,7 +48,7 @@ struct LinearLayout {
     // bfloat16: [rows][ldk or ldn]. FP32: two float16 parts of each; X (for Y by rows, for dW by columns), W by rows, dZ by rows
     // for dX and by columns for dW
     long long x_off, w_off, dz_off, dzc_off;
-    long long xs_off, ws_off, dzs_off, dzcs_off;  // what undoes their scaling: of X's rows or columns, W's rows, dZ's rows and columns
+    long long xs_off, ws_off, dzs_off, dzcs_off;  // the roots of what undoes their scaling: of X's rows or columns, W's rows, dZ's rows and columns
     long long db_off, most_off, mostx_off;        // of strips of kLinearStrip rows: dZ's columns' sums, and the largest values of
                                                   // dZ's and X's columns, [strips][N or K]
     int strips;
@@ -80,11 +80,11 @@ cudaError_t launch_linear_few(const LinearFewParams &p, int dtype, bool vec, int
 // largest finite |x| (most); what is NULL is not made.
 cudaError_t launch_linear_strips(int M, int N, int dtype, const void *src, long long ld, const void *slope, long long lds, void *dz,
                                  long long ldz, float *sums, float *most, bool dependent, cudaStream_t stream);
-// db = the strips' sums + beta * db; what undoes the scaling of columns by their strips' largest values (NULL: not made).
+// db = the strips' sums + beta * db; the root of what undoes the scaling of columns by their strips' largest values (NULL: not made).
 cudaError_t launch_linear_columns(int N, int strips, const float *sums, float beta, void *db, int dtype, const float *most,
                                   float *unscale, bool dependent, cudaStream_t stream);
-// FP32 x = src (* slope) as two float16 parts: by_row of x times factor[column], each row scaled by a power of two
-// (row_unscale undoes it); by_column of x scaled by its columns' (column_unscale undoes it); what is NULL is not made.
+// FP32 x = src (* slope) as two float16 parts: by_row of x times factor[column]^2, each row scaled by a power of two
+// (row_unscale^2 undoes it); by_column of x scaled by its columns' (column_unscale^2 undoes it); what is NULL is not made.
 cudaError_t launch_linear_parts(int rows, int cols, const void *src, long long ld, const void *slope, long long lds,
                                 const float *factor, void *by_row, float *row_unscale, const float *column_unscale, void *by_column,
                                 long long ldp, bool dependent, cudaStream_t stream);
@@ -102,7 +102,7 @@ struct LinearProduct {
     float gamma;
     bool out_tma, add_tma;     // 16-byte aligned rows; else element by element
     bool out_vec, add_vec;     // 4 elements at a time where a split tile is put together
-    const float *row_unscale, *col_unscale;  // of FP32 operands' parts: factors of the result's rows and columns (NULL: 1)
+    const float *row_unscale, *col_unscale;  // of FP32 operands' parts: roots of the factors of the result's rows and columns (NULL: 1)
 };
 
 struct LinearParams {

@@ -13,9 +13,9 @@
 // powers of two, a product of them three products of parts, small ones first: the
 // same loop over more slabs. What is scaled is never the sum's index: X and W by rows
 // for Y; for dX dZ by rows, with W's row factors put into it first; for dW dZ and X
-// by columns. An element far below its row's or column's largest has fewer bits, but
-// in the sum it stands next to the largest; what is made of small ones alone is scaled up as a
-// whole. (Three bfloat16 parts, which need no scaling, took six products: a training
+// by columns. An element far below its row's or column's largest has fewer bits: it is
+// held to 2^-39 of that one, which shows where the other operand is 0, or as small, in
+// the largest one's place. (Three bfloat16 parts, which need no scaling, took six products: a training
 // step of 2047 x 3001 x 1531 438 us.) The tensor core truncates its accumulator at every
 // K = 16 step (relative error 4e-6 at K = 4096, all toward zero), which FP32 results
 // would show: their K range is cut into segments that the epilogue warps add in
@@ -372,8 +372,8 @@ __device__ __forceinline__ void add_bias(const E *bias, bool vec, int cols, floa
     }
 }
 
-// What a tile in FP32 multiplies and adds, asked for before its sums are there: a row's factor, and of a warp's (up to 64)
-// columns each lane's two, of factors and bias. (With the factors and the bias loaded where they are used, a tile of 2048 x 2432
+// What a tile in FP32 multiplies and adds, asked for before its sums are there: the root of a row's factor, and of a warp's (up to
+// 64) columns each lane's two, of factors' roots and bias. (With the factors and the bias loaded where they are used, a tile of 2048 x 2432
 // x 1536 left in 14 us, and its products take 20.)
 struct Scales {
     float row, col[2], bias[2];
@@ -490,8 +490,10 @@ __device__ __forceinline__ void leave_tile(const LinearParams &p, const LinearMa
                 const float col = cb < 2 ? scales.col[0] : scales.col[1], b = cb < 2 ? scales.bias[0] : scales.bias[1];
                 const int from = (cb & 1) * C + j * PER;
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    v[i] = fmaf(v[i] * scales.row, __shfl_sync(0xffffffffu, col, from + i), __shfl_sync(0xffffffffu, b, from + i));
+                for (int i = 0; i < PER; ++i) {
+                    const float root = scales.row * __shfl_sync(0xffffffffu, col, from + i);
+                    v[i] = fmaf(v[i] * root, root, __shfl_sync(0xffffffffu, b, from + i));
+                }
             }
             if (sizeof(E) == 2 && bias != nullptr) add_bias(bias + c + j * PER, bias_vec, cols - j * PER, v);
             const uint32_t at = chunk_at(to, lane, j);
@@ -558,7 +560,10 @@ __device__ __forceinline__ void leave_four(const LinearParams &p, const LinearPr
     if constexpr (sizeof(E) == 4) {
         const float f = q.row_unscale[row];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = x[i] * f * (q.col_unscale != nullptr && i < n ? q.col_unscale[c + i] : 1.0f);
+        for (int i = 0; i < 4; ++i) {
+            const float root = f * (q.col_unscale != nullptr && i < n ? q.col_unscale[c + i] : 1.0f);
+            x[i] = x[i] * root * root;
+        }
     }
     E b[4] = {}, r[4] = {};
     if (first && p.bias != nullptr) {

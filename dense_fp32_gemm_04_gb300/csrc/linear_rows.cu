@@ -141,16 +141,24 @@ linear_strips_kernel(int M, int N, const E *__restrict__ src, long long ld, cons
     }
 }
 
-// 2^-s for the s that brings a largest value of `most` into [2^14, 2^15).
-__device__ __forceinline__ float unscale_of(float most)
+// Scaling by powers of two: numbers whose largest is at least 2^e and below 2^(e + 1) take 2^s, s the even number that brings that
+// into [2^14, 2^16). What is kept of it is 2^(-s / 2): a result's factors, of its row and of its column, are squares, and the
+// product of their roots is within FP32's range whatever the operands, as are the sum times it and that times it again, unless
+// the result itself is outside. (The factors one after the other left the range at X = 1e33 with W = 0.02.) s ends at `most`:
+// 126 takes FP32's smallest number to 2^-23, which float16 holds, and keeps the product of two roots above 2^-127.
+__device__ __forceinline__ float root_unscale(int e, int most = 126) { return __int_as_float((127 - min((15 - e) & ~1, most) / 2) << 23); }
+
+// The exponent of a > 0.
+__device__ __forceinline__ int exponent_of(float a)
 {
-    return most > 0.0f ? scalbnf(1.0f, -min(14 - ilogbf(most), 126)) : 1.0f;
+    const bool tiny = a < 1.17549435e-38f;
+    return (__float_as_int(tiny ? a * 16777216.0f : a) >> 23) - (tiny ? 151 : 127);
 }
 
 // 1 / x for a power of two from 2^-126 to 2^126.
 __device__ __forceinline__ float inverse_power(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 
-// The strips' sums put together: db = sum + beta * db; and their largest values: what undoes the columns' scaling. 32 columns a
+// The strips' sums put together: db = sum + beta * db; and their largest values: the root of what undoes the columns' scaling. 32 columns a
 // block, the strips dealt to 8 rows of threads: few columns still have many loads in flight. (Plain loads: the
 // kernel before it in the call wrote them.)
 template <typename E>
@@ -183,7 +191,7 @@ linear_columns_kernel(int N, int strips, const float *sums, float beta, E *db, c
         if (beta != 0.0f) x = fmaf(beta, static_cast<float>(db[c]), x);
         db[c] = static_cast<E>(x);
     }
-    if (most != nullptr) unscale[c] = unscale_of(y);
+    if (most != nullptr) unscale[c] = y > 0.0f ? root_unscale(exponent_of(y)) : 1.0f;
 }
 
 // Two scaled values as two float16 numbers each (22 bits). The first is finite and what is left, infinities and NaN too, is in the
@@ -198,9 +206,9 @@ __device__ __forceinline__ void two_halves(const float (&x)[2], __half *to, long
     *reinterpret_cast<__half2 *>(to + part) = __floats2half2_rn(x[0] - back.x, x[1] - back.y);
 }
 
-// FP32 rows x = src (* slope) as float16 parts, a block per row. by_row: x times factor[column] (if given), scaled for each row
-// such that its largest finite value lies in [2^14, 2^15), what undoes it in row_unscale; by_column: x scaled by the
-// columns' own factors, which linear_columns_kernel left. Rows of ldp elements on 128-byte lines, the second part `rows` of
+// FP32 rows x = src (* slope) as float16 parts, a block per row. by_row: x times factor[column]^2 (if given), scaled for each row
+// such that its largest finite value lies in [2^14, 2^16), the root of what undoes it in row_unscale; by_column: x scaled by the
+// columns' own factors, whose roots linear_columns_kernel left. Rows of ldp elements on 128-byte lines, the second part `rows` of
 // them further on. A thread keeps PAIRS pairs of a row in registers (of up to 16 THREADS
 // columns: the whole row).
 template <bool VEC, int THREADS>
@@ -210,7 +218,7 @@ linear_parts_kernel(int rows, int cols, const float *__restrict__ src, long long
                     long long ldp)
 {
     constexpr int PAIRS = 8;
-    __shared__ float red[THREADS / 32];
+    __shared__ int red[THREADS / 32];
     const long long r = blockIdx.x, part = rows * ldp;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float *s = src + r * ld, *t = slope != nullptr ? slope + r * lds : nullptr;
@@ -238,14 +246,16 @@ linear_parts_kernel(int rows, int cols, const float *__restrict__ src, long long
     };
     float up = 1.0f;
     if (by_row != nullptr) {
-        float most = 0.0f;
+        // by exponents: a product with W's factor may be far outside FP32's range although the result is not
+        constexpr int kNone = -10000;
+        int most = kNone;
         auto look = [&](int c, const float (&v)[2]) {
             float f[2];
             factors(c, f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float a = fabsf(v[e] * f[e]);
-                most = a < kInf ? fmaxf(most, a) : most;
+                const float a = fabsf(v[e]);
+                if (a > 0.0f && a < kInf) most = max(most, exponent_of(a) + 2 * (__float_as_int(f[e]) >> 23) - 254);
             }
         };
 #pragma unroll
@@ -258,26 +268,33 @@ linear_parts_kernel(int rows, int cols, const float *__restrict__ src, long long
             load(c, v);
             look(c, v);
         }
-        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) red[warp] = most;
         __syncthreads();
         most = red[0];
 #pragma unroll
-        for (int w = 1; w < THREADS / 32; ++w) most = fmaxf(most, red[w]);
-        const float back = unscale_of(most);
+        for (int w = 1; w < THREADS / 32; ++w) most = max(most, red[w]);
+        // (with a factor in them these rows' results have no other: its root may be as small as 2^-126)
+        const float back = most == kNone ? 1.0f : root_unscale(most, factor != nullptr ? 252 : 126);
         if (threadIdx.x == 0) row_unscale[r] = back;
         up = inverse_power(back);
     }
     auto leave = [&](int c, const float (&v)[2]) {
         const bool second = c + 1 < cols;
         if (by_row != nullptr) {
-            float f[2];
+            float f[2], y[2];
             factors(c, f);
-            const float y[2] = {v[0] * f[0] * up, v[1] * f[1] * up};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // (a finite number other than 0 never meets these ends and has bits left)
+                const float g = fminf(fmaxf(f[e] * up, 1.17549435e-38f), 8.5070592e37f);
+                y[e] = v[e] * g * g;
+            }
             two_halves(y, by_row + r * ldp + c, part);
         }
         if (by_column != nullptr) {
-            const float y[2] = {v[0] * inverse_power(column_unscale[c]), second ? v[1] * inverse_power(column_unscale[c + 1]) : 0.0f};
+            const float f[2] = {inverse_power(column_unscale[c]), second ? inverse_power(column_unscale[c + 1]) : 1.0f};
+            const float y[2] = {v[0] * f[0] * f[0], second ? v[1] * f[1] * f[1] : 0.0f};
             two_halves(y, by_column + r * ldp + c, part);
         }
     };

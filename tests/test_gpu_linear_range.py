@@ -42,21 +42,24 @@ def off(a, b, dtype):
     """What a product of the rows of a and b may be off by before it is rounded (infinities and NaN taken as 0)."""
     a, b = (x.double().nan_to_num(nan=0.0, posinf=0.0, neginf=0.0).abs() for x in (a, b))
     K, mag = a.shape[1], a @ b.T
-    tol = mag * ((K + 32) * 2.0 ** -24 + 2.0 ** -17)
+    tol = mag * ((K + 32) * 2.0 ** -24 + 2.0 ** -17) + K * 2.0 ** -149  # (each sum is rounded to a multiple of 2^-149 at least)
     if dtype == F32:
         tol += 2.0 ** -38 * (a.max(1, keepdim=True).values * b.sum(1) + a.sum(1, keepdim=True) * b.max(1).values)
     return tol
 
 
-def same(got, want, tol, dtype):
-    """Equal where want is infinite or NaN, else within tol and a rounding; results next to FP32's end may be on either side of it."""
+def same(got, want, tol, dtype, partial=None):
+    """Equal where want is infinite or NaN, else within tol and a rounding; results next to FP32's end may be on either side of it.
+    partial: sum |a||b| of a form that adds unscaled products in FP32. Where that passes FP32's end, so may some of its products or
+    sums, of either sign, and what comes after an infinity is no number that an FP32 sum in any order is held to."""
     most = torch.finfo(dtype).max
     got = got.double()
     half = torch.finfo(dtype).eps / 2
     near = (got - want).abs() <= tol + half * (want.abs() + tol) + 2.0 ** -149
-    past = (want.abs() + tol >= most) & (got.isinf() | near) & (got.sign() == want.sign())
+    past = (want.abs() + tol >= most) & (got.isinf() | near) & ((got.sign() == want.sign()) | (want.abs() <= tol))
     inf = want.isinf() & (got == want)
-    return bool((near | past | inf | (want.isnan() & got.isnan())).all())
+    lost = ~got.isfinite() & (partial >= most) if partial is not None else False
+    return bool((near | past | inf | (want.isnan() & got.isnan()) | lost).all())
 
 
 def product(a, b):
@@ -90,3 +93,50 @@ def test_infinite_operands(h, M, N, K, dtype):
         want = product(a, b)
         assert want.isinf().any() and want.isnan().any()
         assert same(got, want, off(a, b, dtype), dtype)
+
+
+# (X, W, dY) times these: results near both ends of FP32, though single operands and factors are far outside what they give
+SCALES = [(1e33, 0.02, 1e-3), (1e35, 1.0, 1.0), (1e34, 1e-10, 1e-10), (1e-10, 1e34, 1e34), (1e-12, 1e-20, 1e36), (3e-39, 1e33, 1e30),
+          (1e-20, 1e-17, 1e-20), (1e18, 1e18, 1e17), (1e30, 1e-39, 1e-3), (1e-44, 1e36, 1e-36)]
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("M,N,K", FORMS + [(33, 2100, 2048), (40, 1, 1), (17, 4096, 1100), (16, 4096, 1100)])
+def test_finite_results_are_finite(h, M, N, K, scale):
+    """Both sides of the rule for few tokens (16 | 17 where W is large, 32 | 33 where it is small), split and whole tiles."""
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    X, W, dY = (rand(gen, *s) * f for s, f in zip(((M, K), (N, K), (M, N)), scale))
+    b = rand(gen, N) * min(scale[0] * scale[1], 1e37)
+    Y = h.linear(X, W, bias=b)
+    dX, dW, _ = h.linear_grad(X, W, dY, need_db=False)
+    torch.cuda.synchronize()
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
+    for name, got, a, c, add in (("Y", Y, X, W, b.double()), ("dX", dX, dY, W.T, 0.0), ("dW", dW, dY.T, X.T, 0.0)):
+        ref = product(a, c)
+        want = ref + add
+        assert same(got, want, off(a, c, F32) + 2.0 ** -23 * want.abs(), F32), name
+
+
+@pytest.mark.parametrize("M,N,K", FORMS + [(300, 600, 1030)])
+def test_rows_and_columns_of_very_different_sizes(h, M, N, K):
+    """Each row and each column of the operands has a size of its own, over most of FP32's range; dX's rows see the sizes of
+    W's rows in its sum."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    sizes = lambda n, low, high: 10.0 ** (low + (high - low) * torch.rand(n, device="cuda", generator=gen))  # noqa: E731
+    X = rand(gen, M, K) * sizes(M, -36, 36)[:, None]
+    W = rand(gen, N, K) * sizes(N, -36, 36)[:, None]
+    dY = rand(gen, M, N) * sizes(M, -30, 30)[:, None]
+    Y = h.linear(X, W)
+    dX, _, _ = h.linear_grad(X, W, dY, need_dW=False, need_db=False)
+    torch.cuda.synchronize()
+    few = X.double().abs() @ W.double().abs().T if sg.linear_plan(M, N, K, sg.DTYPE_F32).few else None
+    assert same(Y, product(X, W), off(X, W, F32), F32, few)
+    # W's sizes lie in dX's sum, so it is the products' sizes that count: every row of (dY times W's row sizes) has one largest
+    size = W.double().abs().max(1).values
+    assert same(dX, product(dY, W.T), off(dY.double() * size, (W.double() / size[:, None]).T, F32), F32)
+    X = rand(gen, M, K) * sizes(K, -36, 36)
+    dY = rand(gen, M, N) * sizes(N, -36, 36)
+    _, dW, _ = h.linear_grad(X, W, dY, need_dX=False, need_db=False)
+    torch.cuda.synchronize()
+    assert same(dW, product(dY.T, X.T), off(dY.T, X.T, F32), F32)
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
