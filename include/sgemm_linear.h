@@ -31,8 +31,10 @@
  *   - Rows need no alignment beyond their element's; operands whose rows start on 16-byte
  *     boundaries spare a copy into the workspace.
  *
- * Numerics: bfloat16 operands enter the products as they are, accumulated in FP32 (the
- * tensor cores truncate as they accumulate: up to 2^-17 of a sum of terms of one sign);
+ * Numerics: bfloat16 operands enter the products as they are, accumulated in FP32. The
+ * tensor cores truncate every 16 products, so a sum of n products of one sign comes out
+ * too small by up to n 2^-27 of itself (n is K for Y, N for dX, the number of tokens for dW;
+ * measured with alike terms: 8e-6 at n = 4096, 6e-5 at 16384, 3.4e-4 at 65536; terms of random signs stay below 1e-6);
  * bias, activation and residual are applied in FP32 and Y, dX, dW and db rounded once; dZ
  * enters the products rounded to bfloat16. FP32 operands enter the tensor cores as sums of two float16 parts (22 bits)
  * of rows or columns scaled by powers of two (those that are not the sum's index), 256 products deep at most, the rest

@@ -140,3 +140,37 @@ def test_rows_and_columns_of_very_different_sizes(h, M, N, K):
     torch.cuda.synchronize()
     assert same(dW, product(dY.T, X.T), off(dY.T, X.T, F32), F32)
     assert h.check_device_status() == (sg.SGEMM_OK, 0)
+
+
+def test_deep_sums_of_one_sign(h):
+    """bfloat16 sums of n products of one sign lose up to n 2^-27 of themselves: every 16 products are added to what the sum has
+    reached, half of it on average, and it and they are cut to some 24 bits, together 4 * 2^-24 of it or less. What is near minus
+    the result is added (as residual, as gradient so far), so that the rounding to bfloat16, 2^-8 of what is left, at most
+    (2^-8 + n 2^-27) of the sum, hides none of that. (Means over results would say nothing: such sums differ by 1 / sqrt(n) of
+    themselves, which is less than a step of bfloat16, so their roundings are alike.)"""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    uniform = lambda *s: (0.5 + torch.rand(*s, device="cuda", generator=gen)).to(BF16)  # noqa: E731
+
+    def check(name, n, ref, call):
+        near = -ref.to(BF16)
+        left = call(near.clone())
+        torch.cuda.synchronize()
+        lost = n * 2.0 ** -27
+        rounding = 2.0 ** -8 * (2.0 ** -8 + lost)
+        far = (left.double() - (ref + near.double())) / ref
+        assert -lost - rounding <= far.min().item() and far.max().item() <= rounding, (name, n, far.min().item(), far.max().item())
+
+    for n in (4096, 65536, 300_007):
+        X, dY, W = uniform(n, 200), uniform(n, 264), uniform(264, 200)
+        check("dW", n, dY.double().T @ X.double(), lambda g: h.linear_grad(X, W, dY, dW=g, beta=1.0, need_dX=False, need_db=False)[1])
+        A, B = uniform(150, n), uniform(136, n)
+        check("Y", n, A.double() @ B.double().T, lambda g: h.linear(A, B, residual=g))
+        G, V = uniform(150, n), uniform(n, 136)
+        some = uniform(150, 136)
+        check("dX", n, G.double() @ V.double(), lambda g: h.linear_grad(some, V, G, dX=g, beta=1.0, need_dW=False, need_db=False)[0])
+        _, _, db = h.linear_grad(X, W, dY, need_dX=False, need_dW=False)
+        ref = dY.double().sum(0)
+        assert ((db.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -15) * ref).all()
+    A, B = uniform(2600, 16384), uniform(2304, 16384)  # whole tiles
+    check("Y", 16384, A.double() @ B.double().T, lambda g: h.linear(A, B, residual=g))
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
