@@ -4,10 +4,9 @@ deep sums, and how exact FP32 results are.
 Bounds for FP32 operands, per element of a product of a and b, mag = sum |a||b| over K: an operand is two float16 numbers, so it
 is off by 2^-23 of itself, or by 2^-39 of the largest of its row (2^-25, half the last place of a float16 below 2^-14, where that
 largest one lies in [2^14, 2^16)); the product of the two small parts, at most 2^-22 of |a||b|, is left out; sums of 256 products
-are 16 truncations for each of three products of parts, 48 * 2^-23 at most, and K / 256 of them are added in FP32. All together
-2^-17 mag, K 2^-24 mag and 2^-38 (largest |a| of the row * sum |b| + largest |b| * sum |a|). As a whole results are far nearer:
-truncations of 2^-24 on average, of sums that grow from 0, come to 24 * 2^-25 = 2^-20.4 of a sum of one sign, and to less of
-random signs, whose sums are some sqrt(K) of their terms while the parts' errors are as random as they are.
+are cut 16 times, by 4 * 2^-24 of what they have reached at most (the sums of the parts' other two products, 2^-11 of these, come
+first), 2^-18 mag, and K / 256 of them are added in FP32. All together 2^-17 mag, K 2^-24 mag and 2^-38 (largest |a| of the row *
+sum |b| + largest |b| * sum |a|). As a whole results are nearer, as sums grow from 0 and most cuts are smaller.
 """
 
 import itertools
@@ -174,3 +173,52 @@ def test_deep_sums_of_one_sign(h):
     A, B = uniform(2600, 16384), uniform(2304, 16384)  # whole tiles
     check("Y", 16384, A.double() @ B.double().T, lambda g: h.linear(A, B, residual=g))
     assert h.check_device_status() == (sg.SGEMM_OK, 0)
+
+
+@pytest.mark.parametrize("M,N,K", FORMS + [(24, 2048, 4096), (300, 600, 8192), (2047, 3001, 1531), (64, 1000, 30000)])
+def test_fp32_results_as_a_whole(h, M, N, K):
+    """What the header says of FP32 results, in both math modes, which compute them alike."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    for sign in (False, True):
+        X, W, dY = (rand(gen, *s) for s in ((M, K), (N, K), (M, N)))
+        if sign:
+            X, W, dY = X.abs(), W.abs(), dY.abs()
+        most = 1.5e-6 if sign else 5e-7
+        got = (h.linear(X, W),) + h.linear_grad(X, W, dY, need_db=False)[:2]
+        h.set_math_mode(1)
+        try:
+            other = (h.linear(X, W),) + h.linear_grad(X, W, dY, need_db=False)[:2]
+        finally:
+            h.set_math_mode(0)
+        torch.cuda.synchronize()
+        for name, g, o, a, b in zip(("Y", "dX", "dW"), got, other, (X, dY, dY.T), (W, W.T, X.T)):
+            assert torch.equal(g, o), name
+            ref = product(a, b)
+            assert (g.double() - ref).norm() <= most * ref.norm(), name
+            assert same(g, ref, off(a, b, F32), F32), name
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
+
+
+@pytest.mark.parametrize("M,N,K", FORMS[1:])
+def test_small_elements_beside_large_ones(h, M, N, K):
+    """One element of a row 2^e times the others, the other operand 0 in its place: the others are held to 2^-39 of it, so to
+    2^(e - 39) of themselves, and are gone from e = 40 on. A few tokens lose nothing."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    for e in (10, 25, 32, 45):
+        X, W, dY = ((1.0 + 0.5 * torch.rand(*s, device="cuda", generator=gen)) for s in ((M, K), (N, K), (M, N)))
+        X[:, 3] *= 2.0 ** e
+        W[:, 3] = 0.0
+        dY[5] *= 2.0 ** e
+        X0 = X.clone()
+        X0[5] = 0.0
+        few = h.linear(X[:3], W)
+        Y = h.linear(X, W)
+        dX, _, _ = h.linear_grad(X, W, dY, need_dW=False, need_db=False)
+        _, dW, _ = h.linear_grad(X0, W, dY, need_dX=False, need_db=False)
+        torch.cuda.synchronize()
+        for name, got, a, b in (("Y", Y, X, W), ("dX", dX, dY, W.T), ("dW", dW, dY.T, X0.T)):
+            assert same(got, product(a, b), off(a, b, F32), F32), (name, e)
+        ref = product(X[:3], W)
+        assert (few.double() - ref).norm() <= 5e-7 * ref.norm()
+        if e >= 45:
+            assert (Y == 0).all()
