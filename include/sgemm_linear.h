@@ -13,7 +13,8 @@
  *   slope    act'(X W^T + b), M x N, which the forward call leaves where it is asked
  *            for and the gradients read: FP32 for FP32 operands; for bfloat16 operands
  *            16-bit integers in units of 2^-14 (-32768: NaN). Slopes lie in
- *            [-0.13, 1.13], so a unit is finer than bfloat16 is near 1, and the
+ *            [-0.13, 1.13]: a unit is finer than bfloat16 from 2^-7 on, coarser
+ *            below, and slopes below 2^-15, in the activations' tails, are 0. The
  *            gradients need neither the pre-activation nor the activation again.
  *
  *   gradients (sgemm_linear_grad), from dY and with dZ = dY * slope (dZ = dY without one):
@@ -33,16 +34,20 @@
  *
  * Numerics: bfloat16 operands enter the products as they are, accumulated in FP32. The
  * tensor cores truncate every 16 products, so a sum of n products of one sign comes out
- * too small by up to n 2^-27 of itself (n is K for Y, N for dX, the number of tokens for dW;
- * measured with alike terms: 8e-6 at n = 4096, 6e-5 at 16384, 3.4e-4 at 65536; terms of random signs stay below 1e-6);
- * bias, activation and residual are applied in FP32 and Y, dX, dW and db rounded once; dZ
- * enters the products rounded to bfloat16. FP32 operands enter the tensor cores as sums of two float16 parts (22 bits)
- * of rows or columns scaled by powers of two (those that are not the sum's index), 256 products deep at most, the rest
- * added in FP32: a result is off by less than 5e-7 of its 2-norm where its terms are of random signs, 1.5e-6 where they are
- * of one, whatever the math mode. An element is held to 2^-39 of the largest in its row (X, W and dZ for Y and dX) or
- * column (dZ and X for dW), which shows where the other operand is 0, or as small, in the largest one's place.
- * Infinities and NaN give what the formula has (an element that is held as 0 counts as one beside an infinity). A few
- * tokens are computed without tensor cores, in FP32 fused multiply-adds.
+ * too small by up to n 2^-27 of itself (n is K for Y, N for dX, the number of tokens for
+ * dW; measured with alike terms: 8e-6 at n = 4096, 6e-5 at 16384, 3.4e-4 at 65536; terms
+ * of random signs stay below 1e-6). Bias, activation and residual are applied in FP32, the
+ * activation within 2^-11 of itself, and Y, dX, dW and db rounded once; dZ enters the
+ * products rounded to bfloat16.
+ * FP32 operands enter the tensor cores as sums of two float16 parts (22 bits) of rows or
+ * columns scaled by powers of two (those that are not the sum's index), 256 products deep
+ * at most, the rest added in FP32: a result is off by less than 5e-7 of its 2-norm where
+ * its terms are of random signs, 1.5e-6 where they are of one, whatever the math mode. An
+ * element is held to 2^-39 of the largest in its row (X, W and dZ for Y and dX) or column
+ * (dZ and X for dW), which shows where the other operand is 0, or as small, in the largest
+ * one's place. Infinities and NaN give what the formula has (an element that is held as 0
+ * counts as one beside an infinity). A few tokens are computed without tensor cores, in
+ * FP32 fused multiply-adds.
  * Results are bitwise reproducible for a fixed shape, alignment and plan.
  *
  * Errors: sgemm_status values as for sgemm_run; an invalid argument touches nothing.

@@ -19,6 +19,8 @@ import dense_fp32_gemm_04_gb300 as sg
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
+import layers_reference as lr  # noqa: E402
+
 BF16, F32 = torch.bfloat16, torch.float32
 # few tokens, tiles split over clusters, whole tiles
 FORMS = [(3, 300, 200), (150, 520, 200), (2200, 2400, 192)]
@@ -222,3 +224,19 @@ def test_small_elements_beside_large_ones(h, M, N, K):
         assert (few.double() - ref).norm() <= 5e-7 * ref.norm()
         if e >= 45:
             assert (Y == 0).all()
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_bfloat16_activations_are_rounded_once(h, act):
+    """Also where they are small: the tails are off by less than 2^-10.9 of themselves before they are rounded (2^-11 of the
+    approximation; the exponent, up to 126, is rounded twice, by 2^-24 of itself, and 126 * 2^-23 log(2) is 2^-16.6). Down to
+    z = -12.8, where the normal distribution's density is still above FP32's smallest normal number."""
+    z = torch.cat([torch.linspace(-12.8, 12.8, 40001), -torch.logspace(-30, 1, 2000, base=2.0)]).cuda().to(BF16).unique()
+    z = z[z >= -12.8][:, None].contiguous()
+    one = torch.ones(1, 1, device="cuda", dtype=BF16)
+    for rows in (z, *z.split(3)[::97]):
+        Y = h.linear(rows, one, act=act)
+        torch.cuda.synchronize()
+        y, _ = lr.act(rows.double(), act)
+        low = torch.finfo(F32).tiny * rows.double().abs().clamp_min(1)  # z times a factor that is flushed to 0 below 2^-126
+        assert ((Y.double() - y).abs() <= (2.0 ** -8 + 2.0 ** -10.9) * y.abs() + low).all(), act
