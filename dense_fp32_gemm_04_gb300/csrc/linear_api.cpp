@@ -52,7 +52,7 @@ LinearProblem problem(const Call &c, bool grad)
     const int align = (rows_on(c.X, c.ldx, c.size(), 16) ? 1 : 0) | (rows_on(c.W, c.ldw, c.size(), 16) ? 2 : 0) |
                       (rows_on(c.dY, c.lddy, c.size(), 16) ? 4 : 0);
     return LinearProblem{c.M, c.N, c.K, c.dtype, grad, c.dX != nullptr, c.dW != nullptr, c.db != nullptr, c.slope != nullptr,
-                         align, c.h->num_sms, c.h->math_mode, c.h->linear_pairs,
+                         align, c.h->num_sms, c.h->linear_pairs,
                          c.h->linear_ok ? c.h->linear_clusters : nullptr};
 }
 

@@ -23,7 +23,6 @@ struct LinearProblem {
     bool dx, dw, db, slope;  // gradients asked for, and whether dZ differs from dY
     int align_flags;         // as sgemm_linear_plan's
     int num_sms;
-    int math_mode;
     int pairs;               // CTA pairs resident at once (0: num_sms / 2; < 0: none)
     const int *clusters;     // clusters of 1, 2, .. kLinearMaxSplits CTAs resident at once (NULL: as measured on a GB300)
 };
@@ -122,10 +121,10 @@ struct LinearParams {
     long long timeout_ns;
 };
 
-// Operands in boxes of 64 x 64 of 16-bit elements, b of kind Y of 64 x the columns a CTA has of a tile; results and what is added to them in boxes of 128 bytes x 32 rows (valid maps
-// that are not used where the products' flags say so).
+// Operands in boxes of 64 x 64 of 16-bit elements, b of kind Y of 64 x the columns a CTA has of a tile; results in boxes of
+// 64 bytes x 32 rows (valid maps that are not used where the products' flags say so).
 struct LinearMaps {
-    CUtensorMap a[2], b[2], out[2], add[2], slope;
+    CUtensorMap a[2], b[2], out[2], slope;
 };
 
 cudaError_t linear_set_attributes();

@@ -62,7 +62,6 @@ int validate_linear(const LinearProblem &q)
     if (q.M < 0 || q.N < 1 || q.K < 1) return SGEMM_ERR_INVALID_VALUE;
     if (q.dtype != SGEMM_DTYPE_F32 && q.dtype != SGEMM_DTYPE_BF16) return SGEMM_ERR_INVALID_VALUE;
     if (q.align_flags < 0 || q.align_flags > 7 || q.num_sms < 1) return SGEMM_ERR_INVALID_VALUE;
-    if (q.math_mode != SGEMM_MATH_FP32 && q.math_mode != SGEMM_MATH_TF32) return SGEMM_ERR_INVALID_VALUE;
     // tiles and coordinates are counted in 32 bits
     const long long tiles_m = q.M / 128 + 1LL, tiles_n = q.N / 128 + 1LL, tiles_k = q.K / 128 + 1LL;
     for (long long x : {tiles_m * tiles_n, tiles_m * tiles_k, tiles_n * tiles_k})
@@ -150,8 +149,9 @@ extern "C" int sgemm_linear_plan(int M, int N, int K, int dtype, int grad, int a
 {
     using namespace sgemm_impl;
     if (out == nullptr || (grad != 0 && grad != 1)) return SGEMM_ERR_INVALID_VALUE;
+    if (math_mode != SGEMM_MATH_FP32 && math_mode != SGEMM_MATH_TF32) return SGEMM_ERR_INVALID_VALUE;
     const bool g = grad != 0;
-    const LinearProblem q{M, N, K, dtype, g, g, g, g, g, align_flags, num_sms, math_mode, 0, nullptr};
+    const LinearProblem q{M, N, K, dtype, g, g, g, g, g, align_flags, num_sms, 0, nullptr};
     const int rc = validate_linear(q);
     if (rc != SGEMM_OK) return rc;
     // (a call for some of the gradients takes some of the parts; none of them depends on the pairs or the clusters)

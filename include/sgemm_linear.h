@@ -108,7 +108,7 @@ typedef struct sgemm_linear_plan_s {
  * Host-only planning: what the calls above do on a GPU with `num_sms` SMs. grad: 0 for the layer, 1 for its
  * gradients (all of them, with a slope; workspace_bytes is enough for any of them too, and for any number of CTA pairs
  * that the GPU holds at once). align_flags: bit 0 = rows of X are 16-byte aligned (base and row stride), bit 1 = rows of W, bit
- * 2 = rows of dY. Needs no GPU.
+ * 2 = rows of dY. math_mode: a handle's, as for the other plans; layers are computed alike in all. Needs no GPU.
  */
 int sgemm_linear_plan(int M, int N, int K, int dtype, int grad, int align_flags, int num_sms, int math_mode,
                       sgemm_linear_plan_t *out);
