@@ -43,9 +43,9 @@
  * columns scaled by powers of two (those that are not the sum's index), 256 products deep
  * at most, the rest added in FP32: a result is off by less than 5e-7 of its 2-norm where
  * its terms are of random signs, 1.5e-6 where they are of one, whatever the math mode. An
- * element is held to 2^-39 of the largest in its row (X, W and dZ for Y and dX) or column
- * (dZ and X for dW), which shows where the other operand is 0, or as small, in the largest
- * one's place. Infinities and NaN give what the formula has (an element that is held as 0
+ * element is held to 2^-39 of the largest in its row (X and W for Y; W, and dZ times the
+ * sizes of W's rows, for dX) or column (dZ and X for dW), which shows where the other
+ * operand is 0, or as small, in the largest one's place. Infinities and NaN give what the formula has (an element that is held as 0
  * counts as one beside an infinity). A few tokens are computed without tensor cores, in
  * FP32 fused multiply-adds.
  * Results are bitwise reproducible for a fixed shape, alignment and plan.
