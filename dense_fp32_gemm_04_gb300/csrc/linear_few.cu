@@ -4,14 +4,14 @@
 // them to fill the machine), so the tokens' elements, which come from the first-level
 // cache, are used ROWS times.
 //
-// Bound by W's bytes for one or two tokens (8192 x 2048 in bfloat16, W from memory: 7.6 us, 4.4 TB/s with the launch, 6.4 where
+// Bound by W's bytes for one or two tokens (8192 x 2048 in bfloat16, W from memory: 7.7 us, 4.4 TB/s with the launch, 5.1 where
 // the L2 holds it), by the multiplications from some 8 on. Against the tensor cores, which take as long for 1 token as for 100,
-// in us, here / there:
-//   bfloat16  8192 x 2048    1 token 7.6 / 14.8   4 tokens 10.5 / 13.7   5 tokens 14.7 / 13.7
-//             2048 x 8192    1 token 9.3 / 17.3   4 tokens 10.6 / 16.4   5 tokens 14.6 / 14.5
-//             16384 x 4096   1 token 23.6 / 35.3  4 tokens 31.9 / 32.8   5 tokens 41.2 / 35.6
-//   FP32      4096 x 4096    1 token 14.0 / 58.9  16 tokens 36.5 / 47.1  24 tokens 54.5 / 47.1   32 tokens 67.1 / 47.3
-//             1000 x 1000    1 token 3.3 / 14.2   16 tokens 5.2 / 14.1   32 tokens 7.3 / 14.1
+// in us, here / there, W from memory:
+//   bfloat16  8192 x 2048    1 token 7.7 / 15.2   4 tokens 10.4 / 13.8   5 tokens 14.3 / 13.9
+//             2048 x 8192    1 token 9.0 / 17.1   4 tokens 10.4 / 15.6   5 tokens 14.3 / 14.8
+//             16384 x 4096   1 token 23.0 / 36.7  4 tokens 31.9 / 34.5   5 tokens 41.4 / 33.4
+//   FP32      4096 x 4096    1 token 13.4 / 55.0  16 tokens 47.1 / 44.0 (36.5 / 44.0 with W in the L2)  24 tokens 71.4 / 44.0
+//             1000 x 1000    1 token 4.9 / 14.4   16 tokens 8.1 / 14.6   32 tokens 12.7 / 14.7
 // so up to 4 tokens in bfloat16 and 16 in FP32, and up to 32 where W is small: there (FP32 operands become parts first) the tile
 // kernel takes 13 us and 2 us per million elements of W, these warps 3 us and M / 8 per million.
 #include <cuda_bf16.h>

