@@ -29,6 +29,7 @@ int check(const sgemm_tensor_t &t)
     const unsigned size = t.dtype == SGEMM_DTYPE_BF16 ? 2 : 4;
     if (t.data == nullptr || !aligned(t.data, size) || !aligned(t.out, size)) return SGEMM_ERR_INVALID_VALUE;
     if (t.rows > 1 && (t.ld < t.cols || (t.out != nullptr && t.ld_out < t.cols))) return SGEMM_ERR_INVALID_VALUE;
+    if (t.out == t.data && t.rows > 1 && t.ld_out != t.ld) return SGEMM_ERR_INVALID_VALUE;  // rows over each other
     // every offset counts in 64 bits
     const long long most = 1LL << 60, ld = std::max(t.ld, t.out != nullptr ? t.ld_out : 0);
     if (t.cols > most || (t.rows > 1 && (ld > most || t.rows > most / ld))) return SGEMM_ERR_INVALID_VALUE;
@@ -140,13 +141,14 @@ int sgemm_clip(sgemm_handle_s *h, int count, const sgemm_tensor_t *tensors, floa
     try {
         std::vector<ClipTensor> all;
         std::vector<int> chunks;
-        std::vector<const void *> outs;
+        std::vector<const void *> firsts;  // first elements of tensors and of outputs of their own
         double elements = 0.0;
         for (int i = 0; i < count; ++i) {
             const sgemm_tensor_t &t = tensors[i];
             if (t.rows == 0 || t.cols == 0) continue;
             all.push_back(describe(t));
-            outs.push_back(all.back().out);
+            firsts.push_back(t.data);
+            if (all.back().out != t.data) firsts.push_back(all.back().out);
             elements += static_cast<double>(t.rows) * static_cast<double>(t.cols);
         }
         int chunk = kClipMost;
@@ -158,8 +160,8 @@ int sgemm_clip(sgemm_handle_s *h, int count, const sgemm_tensor_t *tensors, floa
             if (total > 1LL << 30) return SGEMM_ERR_NOT_SUPPORTED;  // chunks are counted in 32 bits
             chunks.push_back(static_cast<int>(n));
         }
-        std::sort(outs.begin(), outs.end());
-        if (std::adjacent_find(outs.begin(), outs.end()) != outs.end()) return SGEMM_ERR_INVALID_VALUE;
+        std::sort(firsts.begin(), firsts.end());
+        if (std::adjacent_find(firsts.begin(), firsts.end()) != firsts.end()) return SGEMM_ERR_INVALID_VALUE;
         DeviceGuard g(h->device);
         if (!g.ok) return SGEMM_ERR_CUDA;
         long long bytes = 0;

@@ -18,7 +18,8 @@
  *   - out == NULL: in place. Otherwise out has the same rows, cols and type, a stride of
  *     its own (ld_out), and is written always, also with a factor of 1.
  *   - Tensors and outputs must not overlap each other, but for an output that is its own
- *     tensor (same address and stride). A tensor named twice is refused.
+ *     tensor (same address and stride). A tensor or an output named twice, or an output that
+ *     starts where another tensor does, is refused; other overlaps are not looked for.
  *   - No tensors, or none with an element: norm = 0.
  *   - max_norm = infinity: the factor is 1 whatever the norm; max_norm = 0: factor 0.
  *   - A norm that is infinite makes the factor 0 (infinite elements become NaN), one that is

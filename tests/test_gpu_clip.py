@@ -164,3 +164,19 @@ def test_refusals(h):
             call()
     torch.cuda.synchronize()
     assert (g == 1).all()
+
+
+def test_tensors_over_each_other_are_refused(h):
+    """Named twice, written over another tensor, or over its own with other rows: nothing is touched."""
+    g, f, o = (torch.full((40, 6), x, device="cuda") for x in (1.0, 2.0, 3.0))
+    for call in (lambda: h.clip_grads([g, g], 0.5, out=[o, f]), lambda: h.clip_grads([g, f], 0.5, out=[f, o]),
+                 lambda: h.clip_grads([g, f], 0.5, out=[o, o]), lambda: h.clip_grads([g, f], 0.5, out=[f, g]),
+                 lambda: h.clip_grads([g[:, :3]], 0.5, out=[g.view(-1)[:120].view(40, 3)])):
+        with pytest.raises(sg.SgemmError):
+            call()
+    torch.cuda.synchronize()
+    assert (g == 1).all() and (f == 2).all() and (o == 3).all()
+    h.clip_grads([g, f], math.inf, out=[g, o])                       # its own tensor, and another one
+    h.clip_grads([g[:, :3], g[:, 3:], f[:0], f[:0]], math.inf)       # neighbours, and tensors without elements
+    torch.cuda.synchronize()
+    assert (g == 1).all() and (f == 2).all() and (o == 2).all()
