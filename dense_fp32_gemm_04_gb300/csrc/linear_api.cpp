@@ -74,6 +74,23 @@ bool kernels_ready(sgemm_handle_t h)
     return h->linear_ok;
 }
 
+// An output that starts where something that the call reads or another output does, Y on R in the same rows apart.
+bool over_each_other(const Call &c, bool grad)
+{
+    const void *const outs[] = {c.Y, grad ? nullptr : c.slope, c.dX, c.dW, c.db};
+    const void *const read[] = {!grad || c.dW != nullptr ? c.X : nullptr, !grad || c.dX != nullptr ? c.W : nullptr, c.bias, c.R, c.dY,
+                                grad ? c.slope : nullptr};
+    for (const void *o : outs) {
+        if (o == nullptr) continue;
+        for (const void *p : read)
+            if (o == p && !(o == c.Y && p == c.R && (c.M <= 1 || c.ldy == c.ldr))) return true;
+        int same = 0;
+        for (const void *p : outs) same += p == o;
+        if (same > 1) return true;
+    }
+    return false;
+}
+
 int check(const Call &c, bool grad)
 {
     if (c.h == nullptr) return SGEMM_ERR_INVALID_VALUE;
@@ -91,6 +108,7 @@ int check(const Call &c, bool grad)
         return SGEMM_ERR_INVALID_VALUE;
     if (c.M > 0 && ((need_x && c.X == nullptr) || (need_w && c.W == nullptr) || (grad ? c.dY == nullptr : c.Y == nullptr)))
         return SGEMM_ERR_INVALID_VALUE;
+    if (c.M > 0 && over_each_other(c, grad)) return SGEMM_ERR_INVALID_VALUE;
     return rc;
 }
 

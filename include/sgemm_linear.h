@@ -25,7 +25,8 @@
  *   - All pointers are DEVICE pointers, everything runs asynchronously on `stream`, in
  *     the handle's workspace; a handle is used by one stream at a time, as with sgemm_run.
  *   - Y may be R itself (same address and row stride): the residual is added in place.
- *     Else outputs overlap neither inputs nor each other.
+ *     Else outputs overlap neither what the call reads nor each other; those that start at
+ *     the same address are refused, other overlaps are not looked for.
  *   - beta == 0: dX, dW and db are written without being read. Any of them may be NULL:
  *     that gradient is not computed.
  *   - M == 0: the layer does nothing; the gradients give dW = beta dW and db = beta db.

@@ -329,3 +329,33 @@ def test_refusals(h):
     assert grad() == sg.SGEMM_OK  # nothing asked for
     torch.cuda.synchronize()
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 48])
+def test_outputs_over_operands_are_refused(h, M, dtype):
+    """And nothing is touched; Y on the residual's own rows, and gradients over what the call does not read, are fine."""
+    X, W, b, R, dY = real(M, 48, 48, dtype, 9)
+    S = real(48, 48, 48, dtype, 10)[0]
+    slope = h.linear(X, W, act="gelu", need_slope=True)[1]
+    given = (X, W, b, R, dY, S)
+    keep = [t.clone() for t in given]
+    wide = torch.zeros(M, 96, device="cuda", dtype=dtype)
+    for call in (lambda: h.linear(X, W, out=X), lambda: h.linear(S, W, residual=S, out=W), lambda: h.linear(X, S, residual=R, out=X),
+                 lambda: h.linear(X, W, residual=wide[:, :48], out=wide.view(-1)[:M * 48].view(M, 48)),
+                 lambda: h.linear_grad(X, W, dY, dX=dY), lambda: h.linear_grad(X, W, dY, dX=X), lambda: h.linear_grad(X, W, dY, dW=W),
+                 lambda: h.linear_grad(S, W, S, dX=W, need_dW=False), lambda: h.linear_grad(S, S, dY=W, dX=S, dW=S)):
+        with pytest.raises(sg.SgemmError):
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, k) for t, k in zip(given, keep)) and (wide == 0).all()
+    want = h.linear_grad(X, W, dY, slope)
+    Y = h.linear(X, W, residual=R)
+    assert h.linear(X, W, residual=R, out=R) is R
+    h.linear_grad(X, W, dY, slope, dW=W, need_dX=False, need_db=False)   # W is not read for dW
+    torch.cuda.synchronize()
+    assert torch.equal(R, Y) and torch.equal(W, want[1])
+    W.copy_(keep[1])
+    h.linear_grad(X, W, dY, slope, dX=X, need_dW=False, need_db=False)   # nor X for dX
+    torch.cuda.synchronize()
+    assert torch.equal(X, want[0]) and h.check_device_status() == (sg.SGEMM_OK, 0)
