@@ -143,6 +143,26 @@ def test_rows_and_columns_of_very_different_sizes(h, M, N, K):
     assert h.check_device_status() == (sg.SGEMM_OK, 0)
 
 
+@pytest.mark.parametrize("M,N,K", FORMS + [(130, 2301, 300)])
+def test_zero_gradients_beside_large_weights(h, M, N, K):
+    """Zeros of dZ (relu's slopes) stand where W's rows are large: dX is made of small rows alone, and is held as they are."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    W, dY = rand(gen, N, K), rand(gen, M, N)
+    large = torch.rand(N, device="cuda", generator=gen) < 0.5
+    large[0] = True
+    W *= torch.where(large, 1e30, 1e-8)[:, None]
+    dY *= 1e-20
+    dY[:, large] = 0.0
+    slope = (torch.rand(M, N, device="cuda", generator=gen) < 0.7).float()
+    dX, _, _ = h.linear_grad(rand(gen, M, K), W, dY, slope, need_dW=False, need_db=False)
+    torch.cuda.synchronize()
+    assert h.check_device_status() == (sg.SGEMM_OK, 0)
+    a, b = (dY * slope)[:, ~large], W[~large].T
+    ref = product(a, b)
+    assert (dX.double() - ref).norm() <= 5e-7 * ref.norm()
+    assert same(dX, ref, off(a, b, F32), F32)
+
+
 def test_deep_sums_of_one_sign(h):
     """bfloat16 sums of n products of one sign lose up to n 2^-27 of themselves: every 16 products are added to what the sum has
     reached, half of it on average, and it and they are cut to some 24 bits, together 4 * 2^-24 of it or less. What is near minus
